@@ -1,0 +1,729 @@
+// cached_attn.cuh -- softmax attention of a few new tokens over the paged 8-bit cache (the
+// hybrid's standard attention layer, one decode step).
+//
+//   o_i = sum_j softmax_j(q_i . k_j / sqrt(d)) v_j,   j <= len - n_q + i,   i = 0 .. n_q - 1
+//
+// with k_j = ks * code, v_j = vs * code, the scales ks, vs those of token j's block.
+//
+// What bounds it: HBM.  A cached byte is used for 2 G n_q multiply-adds (G = Hq / Hkv), 8 to 64
+// flops, so every cached byte is read once and all else has to fit under that stream.
+//
+// The work is cut into tiles of 64 cached tokens of one unit (sequence, kv head, tile of query
+// rows); all tiles stand in one line, and each CTA takes an equal stretch of it, however
+// ragged the lengths.  A unit that lies in several stretches is joined by a second small kernel,
+// in the order of the stretches, so results do not depend on timing.
+//
+// In a CTA, a producer warp finds each tile's blocks (32 table entries at a time, two batches
+// ahead) and brings keys and values in with TMA (swizzled, a ring of stages); four consumer warps
+// take 16 tokens of every tile each.  The products run on mma.sync m16n8k16 in fp16: the codes of
+// e4m3 and int8 are exact in fp16, the query row is scaled by a power of two into fp16's range
+// (an fp32 row is split into two fp16 terms, as is the probability), and sums are fp32.  Tokens are the rows of both
+// products,
+//   S^T [tokens x rows] = K Q^T,       O^T [d x rows] += V^T P^T,
+// so that a product is 8 query rows wide (the G heads of a group), not 16, and P^T becomes the second product's operand
+// by one 8 x 8 transpose in registers (movmatrix).  The tensor pipe is a fifth busy; mma.sync
+// is enough, and its operands come straight from the codes' registers, where tcgen05 would need
+// the fp16 values written back to shared memory.
+// The order of d inside the first product and of tokens inside the second is free, so each
+// thread reads 16 consecutive bytes of a row and converts them in place: for the keys, the four
+// bytes of a word are one k-step's elements of a thread; for the values, bytes of the same d
+// from two tokens are paired by a byte permute.
+//
+// Softmax: x = s + log2(vs) in log2 units.  p = 2^(x - m) weighs the value codes directly, and
+// the row sum takes p / vs: one running reference m serves both, whatever the scales.  m is
+// raised only when some x exceeds it by 2^15 (a warp vote per tile; the accumulators are then
+// rescaled); p stays below 2^15, inside fp16, and keeps full fp16 precision 2^29 below that.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "common.cuh"
+#include "kv_cache.cuh"
+#include "sm100.cuh"
+
+namespace liger {
+namespace ca {
+
+using namespace liger::sm100;
+using kvc::KvType;
+using kvc::kE4m3;
+using kvc::kInt8;
+
+constexpr int kTile = 64;              // cached tokens of a stage
+constexpr int kWarps = 4;              // consumer warps; 16 tokens of a tile each
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
+constexpr float kRefBelow = 7.f;       // the reference is set this far below the maximum,
+constexpr float kRaiseAt = 15.f;       // and raised when a score exceeds it by this much
+
+struct Args {
+  const void* q;            // [B, n_q, Hq, d], tokens qstride elements apart
+  const float* scales;      // [n_blocks, Hkv, 2]
+  const int32_t* table;     // [B, width]
+  const int32_t* lens;      // [B]
+  void* out;                // [B, n_q, Hq, d]
+  float* part_ml;           // [2 ctas][2][kMaxRows] references and sums of the parts
+  float* part_o;            // [2 ctas][kMaxRows][d]
+  int4* split;              // [ctas] the unit that a CTA begins and does not end: (sequence, unit, last CTA, 1)
+  uint32_t* err;
+  uint64_t wait_ns;
+  long qstride;
+  float scale_log2;         // log2(e) / sqrt(d)
+  int B, n_q, Hq, Hkv, G, width, n_blocks, lbs;   // blocks of 2^lbs tokens
+  int rows, row_tiles;                            // rows = n_q * G
+};
+constexpr int kMaxRows = 16;           // query rows of a unit
+
+struct StageInfo {
+  int seq, head, row0, tok0;           // kv head, first query row, first cached token
+  int len, flags;                      // tokens of the sequence; kFirst | kLast | kBegins | kEnds
+  int pad0, pad1;
+  float ks[4], lv[4], iv[4];           // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
+};
+enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };   // the first, last tile of this CTA's stretch of the unit / of the unit itself
+
+// Shared memory.  NT: query rows in eights (1 or 2).
+template <typename Tin, int D, int NT>
+struct Smem {
+  static constexpr uint32_t KV = kTile * D;                       // keys (or values) of a tile
+  static constexpr uint32_t Q = 8 * NT * D * sizeof(Tin);
+  static constexpr uint32_t STAGE = 2 * KV + Q;                   // a multiple of 1024
+  static constexpr uint32_t RED = kWarps * 8 * NT * D * 4;        // partial outputs of the warps
+  static constexpr uint32_t ML = kWarps * 8 * NT * 2 * 4;
+  static constexpr int MAX_STAGES = 12;
+  static constexpr uint32_t FIXED = RED + ML + MAX_STAGES * (sizeof(StageInfo) + 16) + 16 + 64;
+  static uint32_t bytes(int stages, int B) { return 1024 + stages * STAGE + FIXED + 4 * (B + 1); }
+};
+
+__device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+__device__ __forceinline__ float2 unpack_f16(uint32_t x) {
+  return __half22float2(*reinterpret_cast<__half2*>(&x));
+}
+
+// The four codes of a word as two fp16 pairs (bytes 0, 1 and bytes 2, 3): exact.
+template <KvType T>
+__device__ __forceinline__ void codes_to_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  if (T == kE4m3) {
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
+  } else {
+    // code + 128 in the low bits of 1024 (fp16 0x6400), then minus 1152
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 off = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t a = __byte_perm(u, 0x64646464u, 0x4140), b = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 x = __hsub2(*reinterpret_cast<__half2*>(&a), off), y = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+    lo = *reinterpret_cast<const uint32_t*>(&x);
+    hi = *reinterpret_cast<const uint32_t*>(&y);
+  }
+}
+
+// Place of row n (0..7) of an operand in its group of eight tokens: 0 1 3 2 4 5 7 6.  With this order
+// the rows that the lanes of one shared-memory wavefront read, both as key rows (two rows
+// by eight 16-byte columns) and as value rows (four rows by two columns), fall into different
+// banks under the TMA swizzle.
+__device__ __forceinline__ int token_of(int n) { return n ^ ((n >> 1) & 1); }
+
+// Byte offset of column `byte` of row `row` of a swizzled tile of D-byte rows.
+template <int D>
+__device__ __forceinline__ uint32_t swz(int row, int byte) {
+  if (D == 128) return (uint32_t)(row * 128 + (byte ^ ((row & 7) << 4)));
+  return (uint32_t)(row * 64 + (byte ^ (((row >> 1) & 3) << 4)));
+}
+
+__device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
+}
+
+// First tile of CTA c's stretch of the line of W tiles.
+__device__ __forceinline__ long long stretch_begin(long long W, int c, int n) { return W * c / n; }
+// The CTA whose stretch holds tile w.
+__device__ __forceinline__ int stretch_of(long long W, long long w, int n) { return (int)(((w + 1) * n - 1) / W); }
+
+template <typename Tin, int D, KvType T, int NT>
+__global__ void __launch_bounds__(kThreads, 2)
+    cached_attn_kernel(const __grid_constant__ CUtensorMap tm, Args a, int stages) {
+  using S = Smem<Tin, D, NT>;
+  constexpr bool kSplit = sizeof(Tin) == 4;                 // fp32: two fp16 terms of q and of p
+  constexpr int kRows = 8 * NT;
+  extern __shared__ __align__(1024) char smem_raw[];
+  char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  char* fixed = smem + stages * S::STAGE;
+  float* red = reinterpret_cast<float*>(fixed);
+  float* red_ml = reinterpret_cast<float*>(fixed + S::RED);
+  StageInfo* info = reinterpret_cast<StageInfo*>(fixed + S::RED + S::ML);
+  uint64_t* full = reinterpret_cast<uint64_t*>(info + S::MAX_STAGES);
+  uint64_t* empty = full + S::MAX_STAGES;
+  uint64_t* joined = empty + S::MAX_STAGES;                           // [2] the warps' parts written / read
+  int* part = reinterpret_cast<int*>(joined + 2);                     // [5] warp sums of the scan
+  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(part + 8);
+  volatile uint32_t* never = abort_flag + 1;
+  int* first = part + 16;                                             // [B + 1] 64-token tiles before each sequence
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (tid == 0) {
+    for (int i = 0; i < stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], kWarps); }
+    mbar_init(&joined[0], kWarps);
+    mbar_init(&joined[1], kWarps);
+    *abort_flag = 0u;
+    *never = 0u;
+    fence_mbar_init();
+    prefetch_tensormap(&tm);
+  }
+  kvc::pdl_launch_next();
+  kvc::pdl_wait_previous();
+
+  const int cap = a.width << a.lbs;
+  auto length = [&](int s) { const int n = a.lens[s]; return n < 0 ? 0 : (n > cap ? cap : n); };
+  // tiles before each sequence: a block scan, each thread over consecutive sequences
+  {
+    const int per = (a.B + kThreads - 1) / kThreads;
+    const int s0 = tid * per, s1 = min(a.B, s0 + per);
+    int sum = 0;
+    for (int s = s0; s < s1; ++s) {
+      const int n = (length(s) + kTile - 1) / kTile;
+      first[s + 1] = n;
+      sum += n;
+    }
+    int x = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += u;
+    }
+    if (lane == 31) part[warp] = x;
+    __syncthreads();
+    int run = x - sum;
+    for (int w = 0; w < warp; ++w) run += part[w];
+    if (tid == 0) first[0] = 0;
+    for (int s = s0; s < s1; ++s) { run += first[s + 1]; first[s + 1] = run; }
+    __syncthreads();
+  }
+  const int units = a.Hkv * a.row_tiles;                     // of one sequence
+  const long long W = (long long)first[a.B] * units;
+  // as many CTAs as there are tiles, so that no stretch is empty (a unit's parts are those of consecutive CTAs)
+  const int cta = blockIdx.x, n_cta = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
+  const long long w0 = cta < n_cta ? stretch_begin(W, cta, n_cta) : W, w1 = cta < n_cta ? stretch_begin(W, cta + 1, n_cta) : W;
+  if (tid == 0) a.split[cta] = make_int4(0, 0, 0, 0);        // (the consumers' barriers order a later write behind this one)
+  const WaitCtx wc{abort_flag, a.err, a.wait_ns};
+
+  if (warp == kWarps) {   // ---------------- producer
+    const int bs = 1 << a.lbs;
+    const int lppt = a.lbs >= 6 ? 0 : 6 - a.lbs, ppt = 1 << lppt;       // blocks of a tile
+    const int box = bs < kTile ? bs : kTile;                            // rows of one copy
+    const int batch = 32 >> lppt;                                       // tiles looked up at once
+    struct Item { int seq, unit, tile, len, id; float ks, vs; bool live; };
+    const int in_tile = lane & (ppt - 1), lane_tile = lane >> lppt;
+    // the lane's entry of the batch of tiles that starts at w: everything but the scales
+    auto find = [&](long long w) {
+      Item it;
+      w += lane_tile;
+      it.live = w < w1;
+      it.seq = it.unit = it.tile = it.len = 0;
+      it.id = -1;
+      it.ks = 0.f;
+      it.vs = 1.f;
+      if (it.live) {
+        const int f = (int)(w / units);
+        int lo = 0, hi = a.B;   // first[lo] <= f < first[hi]
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) >> 1;
+          if (first[mid] <= f) lo = mid;
+          else hi = mid;
+        }
+        const int n = first[lo + 1] - first[lo];
+        const int r = (int)(w - (long long)first[lo] * units);
+        it.seq = lo;
+        it.unit = r / n;
+        it.tile = r - it.unit * n;
+        it.len = length(lo);
+        const int tok = it.tile * kTile + in_tile * box;
+        if (tok < it.len) {
+          const int id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
+          it.id = id < 0 || id >= a.n_blocks ? -1 : id;
+        }
+      }
+      return it;
+    };
+    auto fetch_scales = [&](Item& it) {
+      if (it.id >= 0) {
+        const float2 s = *reinterpret_cast<const float2*>(
+            a.scales + ((size_t)it.id * a.Hkv + it.unit / a.row_tiles) * 2);
+        it.ks = s.x;
+        it.vs = s.y;
+      }
+    };
+    Item cur = find(w0), next = find(w0 + batch);
+    int k = 0;   // tiles issued
+    bool ok = true;
+    for (long long wb = w0; wb < w1 && ok; wb += batch) {
+      if (wb == w0) fetch_scales(cur);   // (used only behind the first tile's copies)
+      fetch_scales(next);
+      const Item later = find(wb + 2 * batch);
+      const int n_here = (int)(w1 - wb < batch ? w1 - wb : batch);
+      for (int t = 0; t < n_here && ok; ++t, ++k) {
+        const int st = k % stages, use = k / stages;
+        if (use > 0) ok = warp_all(mbar_wait(&empty[st], (use - 1) & 1, wc, wsite(1, st, k)));
+        if (!ok) break;
+        const int owner = t << lppt;
+        const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), unit = __shfl_sync(0xffffffffu, cur.unit, owner);
+        const int tile = __shfl_sync(0xffffffffu, cur.tile, owner), len = __shfl_sync(0xffffffffu, cur.len, owner);
+        const int head = unit / a.row_tiles, row0 = (unit - head * a.row_tiles) * kMaxRows;
+        const bool mine = lane_tile == t && cur.id >= 0;
+        const uint32_t live = __ballot_sync(0xffffffffu, mine);
+        const bool opens = tile == 0 || (wb == w0 && t == 0);
+        const int n_rows = min(kRows, a.rows - row0);
+        char* sk = smem + st * S::STAGE;
+        if (lane == 0)
+          mbar_expect_tx(&full[st], __popc(live) * 2 * box * D + (opens ? n_rows * D * (uint32_t)sizeof(Tin) : 0u));
+        __syncwarp();
+        if (mine) {
+          const int z = cur.id * a.Hkv + head;
+          const int y = (tile * kTile) & (bs - 1);
+          tma_load_3d(sk + in_tile * box * D, &tm, &full[st], 0, y, z);
+          tma_load_3d(sk + S::KV + in_tile * box * D, &tm, &full[st], 0, bs + y, z);
+        }
+        if (opens && lane < n_rows) {   // the unit's query rows: (token, head) pairs
+          const int row = row0 + lane, i = row / a.G, g = row - i * a.G;
+          bulk_load(sk + 2 * S::KV + lane * D * sizeof(Tin),
+                    static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(head * a.G + g) * D,
+                    D * sizeof(Tin), &full[st]);
+        }
+        StageInfo& si = info[st];
+        if (lane_tile == t) {   // the scales of this lane's block, for each 16 tokens of it
+          const float lv = log2f(cur.vs), iv = 1.f / cur.vs;
+          for (int e = 0; e < 4 >> lppt; ++e) {
+            const int slot = in_tile * (4 >> lppt) + e;
+            si.ks[slot] = cur.id >= 0 ? cur.ks : 0.f;
+            si.lv[slot] = lv;
+            si.iv[slot] = iv;
+          }
+        }
+        if (lane == 0) {
+          const int n = first[seq + 1] - first[seq];
+          si.seq = seq;
+          si.head = head;
+          si.row0 = row0;
+          si.tok0 = tile * kTile;
+          si.len = len;
+          const bool ends = tile == n - 1;
+          si.flags = (opens ? kFirst : 0) | (ends || wb + t == w1 - 1 ? kLast : 0) | (tile == 0 ? kBegins : 0) |
+                     (ends ? kEnds : 0);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[st]);
+      }
+      cur = next;
+      next = later;
+    }
+    // never leave with copies in flight
+    const WaitCtx dw{never, nullptr, a.wait_ns};
+    for (int i = k > stages ? k - stages : 0; i < k; ++i) mbar_wait(&full[i % stages], (i / stages) & 1, dw);
+    return;
+  }
+
+  // ---------------- consumers: warp w takes tokens 16 w .. 16 w + 15 of each tile
+  const int g = lane >> 2, t4 = lane & 3;
+  // sequences without tokens: zero rows
+  for (int s = cta; s < a.B; s += gridDim.x)
+    if (first[s + 1] == first[s]) {
+      uint4* o = reinterpret_cast<uint4*>(static_cast<Tin*>(a.out) + (size_t)s * a.n_q * a.Hq * D);
+      const int n16 = a.n_q * a.Hq * D * (int)sizeof(Tin) / 16;
+      for (int i = tid; i < n16; i += 32 * kWarps) o[i] = make_uint4(0u, 0u, 0u, 0u);
+    }
+
+  constexpr int KS = D / 16;            // k-steps of the first product
+  constexpr int MT = D / 16;            // 16-row tiles of O^T
+  uint32_t qf[NT][KS][2], ql[kSplit ? NT : 1][kSplit ? KS : 1][2];   // Q^T operands (and the rows' low terms)
+  float o[NT][MT][4];
+  float ref[NT][2], sum[NT][2], rs[NT][2];
+  int lim[NT][2];                       // tokens that a row sees
+  int row0 = 0;
+  bool begins = false;                  // the CTA's stretch of the unit starts with its first tile
+  uint32_t joins = 0;
+  // all consumer warps meet (bounded, as every wait: a warp that gave up frees the others)
+  auto meet = [&](int b, int k) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&joined[b]);
+    return warp_all(mbar_wait(&joined[b], joins & 1, wc, wsite(3, b, k)));
+  };
+  const int n_tiles = (int)(w1 - w0);
+  for (int k = 0; k < n_tiles; ++k) {
+    const int st = k % stages;
+    if (!warp_all(mbar_wait(&full[st], (k / stages) & 1, wc, wsite(2, st, k)))) return;
+    const StageInfo& si = info[st];
+    const char* sk = smem + st * S::STAGE;
+    const char* sv = sk + S::KV;
+    const int flags = si.flags, len = si.len, tok = si.tok0 + 16 * warp;
+    if (flags & kFirst) {
+      row0 = si.row0;
+      begins = (flags & kBegins) != 0;
+      const char* sq = sv + S::KV;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        // row g of this eight: the thread's d are those whose key bytes it reads (16-byte column c = word j / 4)
+        const int row = row0 + 8 * n + g;
+        const bool in = row < a.rows;
+        float x[KS][4];
+        float top = 0.f;
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          const int at = D == 128 ? (2 * t4 + j / 4) * 16 + (j % 4) * 4 : t4 * 16 + j * 4;
+          if (sizeof(Tin) == 2) {
+            const uint2 u = *reinterpret_cast<const uint2*>(sq + ((8 * n + g) * D + at) * 2);
+            x[j][0] = bf16_lo(u.x); x[j][1] = bf16_hi(u.x); x[j][2] = bf16_lo(u.y); x[j][3] = bf16_hi(u.y);
+          } else {
+            const float4 u = *reinterpret_cast<const float4*>(sq + ((8 * n + g) * D + at) * 4);
+            x[j][0] = u.x; x[j][1] = u.y; x[j][2] = u.z; x[j][3] = u.w;
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            x[j][e] = in ? x[j][e] : 0.f;
+            top = fmaxf(top, fabsf(x[j][e]));
+          }
+        }
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        // the row times 2^-e, its maximum in [2^7, 2^8): exact, and elements 2^-21 of it are still normal in fp16
+        int e = (int)(__float_as_uint(top) >> 23) - 127 - 7;
+        e = min(max(e, -119), 119);
+        const float down = __uint_as_float((uint32_t)(127 - e) << 23), up = __uint_as_float((uint32_t)(127 + e) << 23);
+#pragma unroll
+        for (int j = 0; j < KS; ++j) {
+          const float y0 = x[j][0] * down, y1 = x[j][1] * down, y2 = x[j][2] * down, y3 = x[j][3] * down;
+          qf[n][j][0] = pack_f16(y0, y1);
+          qf[n][j][1] = pack_f16(y2, y3);
+          if (kSplit) {
+            const float2 h0 = unpack_f16(qf[n][j][0]), h1 = unpack_f16(qf[n][j][1]);
+            ql[kSplit ? n : 0][kSplit ? j : 0][0] = pack_f16(y0 - h0.x, y1 - h0.y);
+            ql[kSplit ? n : 0][kSplit ? j : 0][1] = pack_f16(y2 - h1.x, y3 - h1.y);
+          }
+        }
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {   // the thread's score columns are rows 2 t4 + c
+          const int r = row0 + 8 * n + 2 * t4 + c;
+          rs[n][c] = __shfl_sync(0xffffffffu, up, (2 * t4 + c) * 4) * a.scale_log2;
+          lim[n][c] = len - a.n_q + r / a.G + 1;
+          ref[n][c] = kNoRef;
+          sum[n][c] = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
+      }
+    }
+    const float ks = si.ks[warp], lv = si.lv[warp], iv = si.iv[warp];
+    if (tok < len && ks != 0.f) {
+      // keys: rows g and g + 8 of the warp's 16 tokens
+      const int r0 = 16 * warp + token_of(g);
+      uint32_t kw[2][KS];
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int c = 0; c < KS / 4; ++c) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + swz<D>(r0 + 8 * r, (D == 128 ? 2 * t4 + c : t4) * 16));
+          kw[r][4 * c] = u.x; kw[r][4 * c + 1] = u.y; kw[r][4 * c + 2] = u.z; kw[r][4 * c + 3] = u.w;
+        }
+      // values: this thread's four tokens, D / 8 bytes at column g
+      uint32_t vw[4][D / 32];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = 16 * warp + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
+        if (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + swz<D>(row, g * 16));
+          vw[r][0] = u.x; vw[r][1] = u.y; vw[r][D / 32 - 2] = u.z; vw[r][D / 32 - 1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(sv + swz<D>(row, g * 8));
+          vw[r][0] = u.x; vw[r][1] = u.y;
+        }
+      }
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < KS; ++j) {
+        uint32_t a0, a1, a2, a3;
+        codes_to_f16<T>(kw[0][j], a0, a2);
+        codes_to_f16<T>(kw[1][j], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          mma16816(s[n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+          if (kSplit)
+            mma16816(s[n], a0, a1, a2, a3, ql[kSplit ? n : 0][kSplit ? j : 0][0], ql[kSplit ? n : 0][kSplit ? j : 0][1]);
+        }
+      }
+      // to log2 units, with the value scale; tokens that a row does not see
+      const bool edge = tok + 16 > len - a.n_q + 1;
+      bool raise = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          s[n][c] = fmaf(s[n][c], ks * rs[n][c & 1], lv);
+          if (edge && tok + 8 * (c >> 1) + token_of(g) >= lim[n][c & 1]) s[n][c] = -INFINITY;
+          raise |= s[n][c] > ref[n][c & 1] + kRaiseAt;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float top = fmaxf(s[n][c], s[n][c + 2]);
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+            const float to = fmaxf(ref[n][c], top - kRefBelow);
+            f[c] = ex2(ref[n][c] - to);
+            ref[n][c] = to;
+            sum[n][c] *= f[c];
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i) {
+            o[n][i][0] *= f[0]; o[n][i][1] *= f[1];
+            o[n][i][2] *= f[0]; o[n][i][3] *= f[1];
+          }
+        }
+      }
+      float p[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) p[n][c] = ex2(s[n][c] - ref[n][c & 1]);
+        sum[n][0] = fmaf(p[n][0] + p[n][2], iv, sum[n][0]);
+        sum[n][1] = fmaf(p[n][1] + p[n][3], iv, sum[n][1]);
+      }
+      // O^T += V^T P^T.  At the sequence's end (edge) there is one pass for each new token, over the value
+      // codes that it sees, and only its rows take the sums: with weights of zero alone, a NaN code behind
+      // a row's last visible token would reach it.
+      auto weigh = [&](auto at_end, int sees) {
+        constexpr bool kEdge = decltype(at_end)::value;
+        uint32_t pb[NT][2], pl[kSplit ? NT : 1][2];   // P^T operands (and their low terms)
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const uint32_t h0 = pack_f16(p[n][0], p[n][1]), h1 = pack_f16(p[n][2], p[n][3]);
+          pb[n][0] = transpose8x8(h0);
+          pb[n][1] = transpose8x8(h1);
+          if (kSplit) {
+            const float2 x = unpack_f16(h0), y = unpack_f16(h1);
+            pl[kSplit ? n : 0][0] = transpose8x8(pack_f16(p[n][0] - x.x, p[n][1] - x.y));
+            pl[kSplit ? n : 0][1] = transpose8x8(pack_f16(p[n][2] - y.x, p[n][3] - y.y));
+          }
+        }
+        bool seen[4];   // of the thread's four tokens
+        if (kEdge)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) seen[r] = tok + 8 * (r >> 1) + token_of(2 * t4 + (r & 1)) < sees;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          const uint32_t v0 = !kEdge || seen[0] ? vw[0][c] : 0u, v1 = !kEdge || seen[1] ? vw[1][c] : 0u;
+          const uint32_t v2 = !kEdge || seen[2] ? vw[2][c] : 0u, v3 = !kEdge || seen[3] ? vw[3][c] : 0u;
+          // bytes of the same d from the tokens of a pair, side by side
+          const uint32_t lo01 = __byte_perm(v0, v1, 0x5140), hi01 = __byte_perm(v0, v1, 0x7362);
+          const uint32_t lo23 = __byte_perm(v2, v3, 0x5140), hi23 = __byte_perm(v2, v3, 0x7362);
+          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+          codes_to_f16<T>(lo01, a0, a1);
+          codes_to_f16<T>(lo23, a2, a3);
+          codes_to_f16<T>(hi01, b0, b1);
+          codes_to_f16<T>(hi23, b2, b3);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            float x[2][4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) { x[0][e] = o[n][2 * c][e]; x[1][e] = o[n][2 * c + 1][e]; }
+            mma16816(x[0], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            mma16816(x[1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+            if (kSplit) {
+              mma16816(x[0], a0, a1, a2, a3, pl[kSplit ? n : 0][0], pl[kSplit ? n : 0][1]);
+              mma16816(x[1], b0, b1, b2, b3, pl[kSplit ? n : 0][0], pl[kSplit ? n : 0][1]);
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (!kEdge || lim[n][e & 1] == sees) { o[n][2 * c][e] = x[0][e]; o[n][2 * c + 1][e] = x[1][e]; }
+          }
+        }
+      };
+      if (!edge) {
+        weigh(std::false_type{}, 0);
+      } else {
+#pragma unroll 1
+        for (int sees = max(len - a.n_q + 1, tok + 1); sees <= len; ++sees) weigh(std::true_type{}, sees);
+      }
+    }
+    const int seq = si.seq, head = si.head, tile = si.tok0 / kTile;
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&empty[st]);
+
+    if (flags & kLast) {
+      // join the four warps' parts of this stretch of the unit
+      const int n_rows = min(kRows, a.rows - row0);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float l = sum[n][c];
+          l += __shfl_xor_sync(0xffffffffu, l, 4);
+          l += __shfl_xor_sync(0xffffffffu, l, 8);
+          l += __shfl_xor_sync(0xffffffffu, l, 16);
+          if (g == 0) {
+            red_ml[(warp * kRows + 8 * n + 2 * t4 + c) * 2] = ref[n][c];
+            red_ml[(warp * kRows + 8 * n + 2 * t4 + c) * 2 + 1] = l;
+          }
+          // O^T: the thread holds d = 2 MT g .. 2 MT g + 2 MT - 1 of the row
+          if (8 * n + 2 * t4 + c < n_rows) {
+            float* dst = red + (size_t)(warp * kRows + 8 * n + 2 * t4 + c) * D + 2 * MT * g;
+#pragma unroll
+            for (int i = 0; i < MT; i += 2)
+              *reinterpret_cast<float4*>(dst + 2 * i) =
+                  make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
+          }
+        }
+      if (!meet(0, k)) return;
+      const bool whole = begins && (flags & kEnds);
+      const bool carries_on = !begins;              // part of a unit that an earlier CTA began
+      const int slot = 2 * cta + (carries_on ? 0 : 1);
+      for (int v = tid; v < n_rows * (D / 4); v += 32 * kWarps) {
+        const int r = v / (D / 4), c = v % (D / 4);
+        float m = kNoRef;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_ml[(w * kRows + r) * 2]);
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(red_ml[(w * kRows + r) * 2] - m);
+          l = fmaf(f, red_ml[(w * kRows + r) * 2 + 1], l);
+          const float4 x = *reinterpret_cast<const float4*>(red + (size_t)(w * kRows + r) * D + 4 * c);
+          acc.x = fmaf(f, x.x, acc.x); acc.y = fmaf(f, x.y, acc.y);
+          acc.z = fmaf(f, x.z, acc.z); acc.w = fmaf(f, x.w, acc.w);
+        }
+        if (whole) {
+          const float il = l == 0.f ? 0.f : 1.f / l;   // (a row that sees nothing is zero)
+          const int row = row0 + r, i = row / a.G, h = head * a.G + row - i * a.G;
+          Tin* dst = static_cast<Tin*>(a.out) + (((size_t)seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
+          if (sizeof(Tin) == 2)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * il, acc.y * il), pack_bf16(acc.z * il, acc.w * il));
+          else
+            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * il, acc.y * il, acc.z * il, acc.w * il);
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kMaxRows + r) * D + 4 * c) = acc;
+          if (c == 0) {
+            a.part_ml[(size_t)slot * 2 * kMaxRows + r] = m;
+            a.part_ml[(size_t)slot * 2 * kMaxRows + kMaxRows + r] = l;
+          }
+        }
+      }
+      if (!whole && !carries_on && tid == 0) {   // the unit goes on in later stretches
+        const long long last = w0 + k + (first[seq + 1] - first[seq]) - 1 - tile;   // its last tile
+        a.split[cta] = make_int4(seq, head * a.row_tiles + row0 / kMaxRows, stretch_of(W, last, n_cta), 1);
+      }
+      if (!meet(1, k)) return;   // the buffers are free again
+      ++joins;
+    }
+  }
+}
+
+// Joins a unit that one CTA of cached_attn_kernel began and did not end: its parts stand in the
+// begin slot of that CTA and in the continue slots of the next ones.  One CTA per CTA of the
+// first kernel; the parts are added in their order.
+constexpr int kJoinThreads = 256;
+template <typename Tin, int D>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
+  extern __shared__ float sh[];
+  const int tid = threadIdx.x;
+  kvc::pdl_launch_next();
+  kvc::pdl_wait_previous();
+  const int c0 = blockIdx.x;
+  const int4 u = a.split[c0];
+  if (!u.w) return;
+  const int head = u.y / a.row_tiles, row0 = (u.y - head * a.row_tiles) * kMaxRows;
+  const int n_rows = min(kMaxRows, a.rows - row0), parts = min(u.z, (int)gridDim.x - 1) - c0 + 1;
+  auto slot_of = [&](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
+  float* wgt = sh;                            // [parts][kMaxRows] 2^(m_part - m) / l
+  float4* acc = reinterpret_cast<float4*>(sh + (size_t)gridDim.x * kMaxRows);   // [kJoinThreads]
+  // weights: eight lanes per row
+  {
+    constexpr int kLanes = 8;
+    const int r = tid / kLanes, e = tid % kLanes;
+    const bool in = r < n_rows;
+    float m = kNoRef, l = 0.f;
+    if (in)
+      for (int p = e; p < parts; p += kLanes) m = fmaxf(m, a.part_ml[(size_t)slot_of(p) * 2 * kMaxRows + r]);
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (in)
+      for (int p = e; p < parts; p += kLanes) {
+        const float* ml = a.part_ml + (size_t)slot_of(p) * 2 * kMaxRows + r;
+        const float f = ex2(ml[0] - m);
+        wgt[p * kMaxRows + r] = f;
+        l = fmaf(f, ml[kMaxRows], l);
+      }
+#pragma unroll
+    for (int o = 1; o < kLanes; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    const float il = l == 0.f ? 0.f : 1.f / l;
+    if (in)
+      for (int p = e; p < parts; p += kLanes) wgt[p * kMaxRows + r] *= il;
+  }
+  __syncthreads();
+  // the sum: `lanes` threads of a float4 of the output each take every lanes-th part
+  const int vecs = n_rows * (D / 4);
+  const int lanes = vecs >= kJoinThreads ? 1 : kJoinThreads / vecs;
+  for (int v0 = 0; v0 < vecs; v0 += kJoinThreads) {
+    const int v = v0 + tid % (lanes > 1 ? vecs : kJoinThreads), e = lanes > 1 ? tid / vecs : 0;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int r = v / (D / 4), c = v % (D / 4);
+    const bool in = v < vecs && e < lanes;
+    if (in)
+#pragma unroll 8
+      for (int p = e; p < parts; p += lanes) {
+        const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((size_t)slot_of(p) * kMaxRows + r) * D + 4 * c);
+        const float f = wgt[p * kMaxRows + r];
+        x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y);
+        x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
+      }
+    if (lanes > 1) {
+      acc[tid] = x;
+      __syncthreads();
+      if (in && e == 0)
+        for (int q = 1; q < lanes; ++q) {
+          const float4 y = acc[q * vecs + v];
+          x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+        }
+    }
+    if (in && e == 0) {
+      const int row = row0 + r, i = row / a.G, h = head * a.G + row - i * a.G;
+      Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.x * a.n_q + i) * a.Hq + h) * D + 4 * c;
+      if (sizeof(Tin) == 2)
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+      else
+        *reinterpret_cast<float4*>(dst) = x;
+    }
+  }
+}
+
+}  // namespace ca
+}  // namespace liger

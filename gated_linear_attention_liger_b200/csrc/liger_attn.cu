@@ -19,6 +19,7 @@
 #include "common.cuh"
 #include "decode.cuh"
 #include "full_attn.cuh"
+#include "hooks.cuh"
 #include "prefill_bwd.cuh"
 #include "prefill_seg.cuh"
 #include "prefill_simt.cuh"
@@ -310,6 +311,13 @@ bool take_injected_stall() {
 
 // Records a failure for liger_last_error() from other translation units of the library.
 void set_last_error(liger_status status, const char* message) { fail(status, "%s", message); }
+void clear_last_error() { g_last_error.clear(); }
+void count_kernel_launches(int n) { count_launches(n); }
+void mark_dominant_start(cudaStream_t s) { mark_start(s); }
+void mark_dominant_stop(cudaStream_t s) { mark_stop(s); }
+int device_sm_count() { return tc::num_sms(); }
+uint64_t bounded_wait_ns() { return tc::wait_limit_ns(); }
+TensorMapEncodeFn tensor_map_encoder() { return tc::encode_fn(); }
 
 // Whether a prefill with these arguments runs on the tensor-core path, the only one that
 // uses the workspace.

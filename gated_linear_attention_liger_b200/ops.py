@@ -18,6 +18,8 @@ LIB_PATH = os.path.join(_PKG, "libliger_attn.so")
 
 LIGER_OK, LIGER_ERR_INVALID_ARG, LIGER_ERR_UNSUPPORTED, LIGER_ERR_CUDA, LIGER_ERR_TIMEOUT = range(5)
 LIGER_BF16, LIGER_FP32 = 0, 1
+LIGER_KV_E4M3, LIGER_KV_INT8 = 0, 1
+KV_CACHE_MAX_NEW = 16        # new tokens a sequence that cached_attention takes
 STATUS_NAMES = {0: "LIGER_OK", 1: "LIGER_ERR_INVALID_ARG", 2: "LIGER_ERR_UNSUPPORTED",
                 3: "LIGER_ERR_CUDA", 4: "LIGER_ERR_TIMEOUT"}
 
@@ -54,6 +56,13 @@ SIGNATURES = {
     "liger_attn_full_causal": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _i, _i, _vp]),
     "liger_attn_full_causal_status": (_i, []),
     "liger_attn_decode_status": (_i, []),
+    "liger_kv_cache_assign": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _vp]),
+    "liger_kv_cache_append": (_i, [_vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, ctypes.c_longlong, ctypes.c_longlong,
+                                   _i, _i, _vp]),
+    "liger_attn_cached_workspace_size": (ctypes.c_size_t, [_i]),
+    "liger_attn_cached": (_i, [_vp, _vp, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, ctypes.c_longlong, _i, _i,
+                               _vp, ctypes.c_size_t, _vp]),
+    "liger_attn_cached_status": (_i, []),
     "liger_set_timing_events": (None, [_vp, _vp]),
     "liger_kernel_launches": (ctypes.c_uint64, []),
 }
@@ -407,3 +416,213 @@ def decode_vector_gate(q, k, v, state, ring, pos, alpha: float = 0.5, out=None, 
         float(alpha), _dt(q), _stream_ptr(stream))
     _check(st)
     return out
+
+
+# ------------------------------------------------------------------ paged 8-bit cache
+
+def _kv_dt(cache: torch.Tensor) -> int:
+    if cache.dtype == torch.float8_e4m3fn:
+        return LIGER_KV_E4M3
+    if cache.dtype == torch.int8:
+        return LIGER_KV_INT8
+    raise TypeError(f"unsupported cache dtype {cache.dtype} (float8_e4m3fn or int8)")
+
+
+class _On:
+    """The device and stream of a call: launches go to `dev` whatever device is current, and what
+    a call allocates belongs to the stream it runs on."""
+    __slots__ = ("dev", "stream", "_inner")
+
+    def __init__(self, dev, stream):
+        self._inner = None
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+            if torch.cuda.current_device() != dev.index:
+                self._inner = torch.cuda.device(dev)
+        else:
+            if stream.device != dev:
+                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+            self._inner = torch.cuda.stream(stream)   # (makes dev current as well)
+        self.stream = ctypes.c_void_p(stream.cuda_stream)
+
+    def __enter__(self):
+        if self._inner is not None:
+            self._inner.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._inner is not None:
+            self._inner.__exit__(*exc)
+        return False
+
+
+def _need_cuda_strided(*ts):
+    """As _need_cuda, for tensors whose layout has been checked apart."""
+    ref = ts[0].device
+    for t in ts:
+        if not t.is_cuda:
+            raise ValueError("tensors must be CUDA tensors")
+        if t.device != ref:
+            raise ValueError(f"tensors must be on one device ({ref} and {t.device})")
+
+
+def _token_stride(t, name, heads, d):
+    """Elements between the tokens of [..., heads, d], heads and elements contiguous, the tokens
+    evenly spaced (a slice of a fused projection, for instance)."""
+    if t.is_contiguous():
+        return heads * d
+    sh, st = t.shape, t.stride()
+    ok = (d == 1 or st[-1] == 1) and (heads == 1 or st[-2] == d)
+    lead = [(n, s) for n, s in zip(sh[:-2], st[:-2]) if n > 1]
+    for (_, outer), (n, inner) in zip(lead, lead[1:]):
+        ok = ok and outer == n * inner
+    if not ok:
+        raise ValueError(f"{name}: heads and elements must be contiguous and tokens evenly spaced, got strides {tuple(st)}")
+    return lead[-1][1] if lead else heads * d
+
+
+def _check_cache(cache, scales):
+    if cache.dim() != 5 or cache.shape[2] != 2:
+        raise ValueError("cache must be [n_blocks, Hkv, 2, block_size, d]")
+    n_blocks, Hkv, _, block_size, d = cache.shape
+    _expect(scales, "scales", (n_blocks, Hkv, 2), torch.float32)
+    if not cache.is_contiguous() or not scales.is_contiguous():
+        raise ValueError("cache and scales must be contiguous")
+    return n_blocks, Hkv, block_size, d, _kv_dt(cache)
+
+
+def kv_cache_new(n_blocks: int, Hkv: int, d: int, block_size: int, max_seqs: int, max_tokens: int,
+                 dtype=torch.float8_e4m3fn, device="cuda") -> dict:
+    """The tensors of an empty paged 8-bit cache for max_seqs sequences of up to max_tokens tokens.
+
+    cache [n_blocks, Hkv, 2, block_size, d] (e4m3 or int8), scales [n_blocks, Hkv, 2] fp32, block_table
+    [max_seqs, ceil(max_tokens / block_size)], seq_lens [max_seqs], free_blocks [n_blocks] and free_span [2]
+    (int32): all blocks free.
+    """
+    i32 = dict(device=device, dtype=torch.int32)
+    cache = torch.zeros(n_blocks, Hkv, 2, block_size, d, device=device, dtype=torch.uint8).view(dtype)
+    _kv_dt(cache)
+    return {"cache": cache, "scales": torch.ones(n_blocks, Hkv, 2, device=device, dtype=torch.float32),
+            "block_table": torch.full((max_seqs, -(-max_tokens // block_size)), -1, **i32),
+            "seq_lens": torch.zeros(max_seqs, **i32), "free_blocks": torch.arange(n_blocks, **i32),
+            "free_span": torch.tensor([0, n_blocks], **i32)}
+
+
+def kv_cache_assign(new_lens, seq_lens, block_table, free_blocks, free_span, block_size: int, n_slots: int,
+                    slot_map=None, cu_new=None, seq_lens_out=None, free_span_out=None, stream=None):
+    """Block tables and slot maps from request lengths (int32 CUDA tensors, all on the device).
+
+    new_lens [B]: tokens to add to each sequence; a negative number ends it and gives its blocks
+    back.  seq_lens [B], block_table [B, width], free_blocks [n_blocks] and free_span [2]: the state
+    (`kv_cache_new`); the table and the ring of free blocks are updated in place.  n_slots: length of the
+    slot map (at least the sum of the new lengths; the rest is -1).  seq_lens_out and free_span_out may be
+    seq_lens and free_span (the state then advances in place).  Returns (slot_map [n_slots], cu_new [B + 1],
+    seq_lens_out, free_span_out).
+    """
+    lib = load()
+    if new_lens.dim() != 1 or block_table.dim() != 2 or free_blocks.dim() != 1:
+        raise ValueError("new_lens must be [B], block_table [B, width] and free_blocks [n_blocks]")
+    B, i32 = new_lens.shape[0], torch.int32
+    if new_lens.dtype != i32 or free_blocks.dtype != i32:
+        raise ValueError("new_lens and free_blocks must be int32")
+    width, n_blocks = block_table.shape[1], free_blocks.shape[0]
+    _expect(seq_lens, "seq_lens", (B,), i32)
+    _expect(block_table, "block_table", (B, width), i32)
+    _expect(free_span, "free_span", (2,), i32)
+    _expect(slot_map, "slot_map", (n_slots,), i32)
+    _expect(cu_new, "cu_new", (B + 1,), i32)
+    _expect(seq_lens_out, "seq_lens_out", (B,), i32)
+    _expect(free_span_out, "free_span_out", (2,), i32)
+    _need_cuda(new_lens, seq_lens, block_table, free_blocks, free_span, slot_map, cu_new, seq_lens_out, free_span_out)
+    dev = new_lens.device
+    with _On(dev, stream) as s:
+        if slot_map is None:
+            slot_map = torch.empty(n_slots, device=dev, dtype=i32)
+        if cu_new is None:
+            cu_new = torch.empty(B + 1, device=dev, dtype=i32)
+        if seq_lens_out is None:
+            seq_lens_out = torch.empty(B, device=dev, dtype=i32)
+        if free_span_out is None:
+            free_span_out = torch.empty(2, device=dev, dtype=i32)
+        st = lib.liger_kv_cache_assign(
+            new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(), free_span.data_ptr(),
+            slot_map.data_ptr(), cu_new.data_ptr(), seq_lens_out.data_ptr(), free_span_out.data_ptr(), B, width, n_blocks,
+            block_size, n_slots, s)
+    _check(st)
+    return slot_map, cu_new, seq_lens_out, free_span_out
+
+
+def kv_cache_append(k, v, slot_map, cache, scales, stream=None):
+    """Quantises keys and values into their slots of the cache (in place).
+
+    k, v [N, Hkv, d] (bf16 or fp32; tokens may be evenly strided), slot_map [N] int32 as
+    `kv_cache_assign` gives it (-1: left out), cache [n_blocks, Hkv, 2, block_size, d], scales
+    [n_blocks, Hkv, 2] fp32.
+    """
+    lib = load()
+    n_blocks, Hkv, block_size, d, kv_dt = _check_cache(cache, scales)
+    if k.dim() != 3:
+        raise ValueError("k and v must be [N, Hkv, d]")
+    N = k.shape[0]
+    _expect(k, "k", (N, Hkv, d), k.dtype)
+    _expect(v, "v", (N, Hkv, d), k.dtype)
+    _expect(slot_map, "slot_map", (N,), torch.int32)
+    if not slot_map.is_contiguous():
+        raise ValueError("slot_map must be contiguous")
+    dt = _dt(k)
+    ks, vs = _token_stride(k, "k", Hkv, d), _token_stride(v, "v", Hkv, d)
+    _need_cuda_strided(k, v, slot_map, cache, scales)
+    with _On(k.device, stream) as s:
+        st = lib.liger_kv_cache_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache.data_ptr(), scales.data_ptr(),
+                                       N, Hkv, d, n_blocks, block_size, ks, vs, dt, kv_dt, s)
+    _check(st)
+
+
+def cached_attention_workspace_size(d: int) -> int:
+    return int(load().liger_attn_cached_workspace_size(d))
+
+
+def cached_attention(q, cache, scales, block_table, seq_lens, out=None, workspace=None, stream=None):
+    """Softmax attention of each sequence's newest tokens over its cached tokens, themselves
+    included (one decode step of the hybrid's standard attention layer).
+
+    q [B, Hq, d], or [B, n_q, Hq, d] for n_q <= 16 new tokens a sequence (bf16 or fp32; tokens may be
+    evenly strided); cache, scales, block_table [B, width] and seq_lens [B] as for `kv_cache_append`, seq_lens
+    with the new tokens counted.  workspace: uint8 CUDA tensor of cached_attention_workspace_size(d)
+    bytes (allocated here when None).  Returns out in q's shape.
+    """
+    lib = load()
+    n_blocks, Hkv, block_size, d, kv_dt = _check_cache(cache, scales)
+    if q.dim() not in (3, 4) or q.shape[-1] != d:
+        raise ValueError(f"q must be [B, Hq, {d}] or [B, n_q, Hq, {d}]")
+    if block_table.dim() != 2 or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be [B, width] int32")
+    B, Hq = q.shape[0], q.shape[-2]
+    n_q = q.shape[1] if q.dim() == 4 else 1
+    width = block_table.shape[1]
+    _expect(block_table, "block_table", (B, width), torch.int32)
+    _expect(seq_lens, "seq_lens", (B,), torch.int32)
+    _expect(out, "out", q.shape, q.dtype)
+    dt = _dt(q)
+    qs = _token_stride(q, "q", Hq, d)
+    for t in (block_table, seq_lens, out, workspace):
+        if t is not None and not t.is_contiguous():
+            raise ValueError("block_table, seq_lens, out and workspace must be contiguous")
+    dev = q.device
+    _need_cuda_strided(q, cache, scales, block_table, seq_lens, *(t for t in (out, workspace) if t is not None))
+    with _On(dev, stream) as s:
+        if out is None:
+            out = torch.empty(q.shape, device=dev, dtype=q.dtype)
+        if workspace is None:
+            workspace = torch.empty(lib.liger_attn_cached_workspace_size(d), device=dev, dtype=torch.uint8)
+        st = lib.liger_attn_cached(
+            q.data_ptr(), cache.data_ptr(), scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+            B, n_q, Hq, Hkv, d, width, n_blocks, block_size, qs, dt, kv_dt, workspace.data_ptr(),
+            workspace.numel() * workspace.element_size(), s)
+    _check(st)
+    return out
+
+
+def cached_attention_status() -> int:
+    """LIGER_OK, or LIGER_ERR_TIMEOUT if a cached attention call gave up waiting since the last query."""
+    return int(load().liger_attn_cached_status())

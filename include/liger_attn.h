@@ -330,6 +330,104 @@ liger_status liger_attn_full_causal(const void* q, const void* k, const void* v,
                                     int max_seqlen, void* stream);
 liger_status liger_attn_full_causal_status(void);
 
+/*
+ * The paged 8-bit key/value cache of the standard attention layer.  (The pages keep one
+ * full softmax attention layer after every seven Liger layers, news article on Liger,
+ * section "ハイブリッドメカニズム", and do not say how it is served; the cache is this
+ * library's.)
+ *
+ *   cache   [n_blocks, Hkv, 2, block_size, d]  8-bit codes: the keys, then the values, of
+ *           block_size tokens.  LIGER_KV_E4M3 (4 exponent, 3 fraction bits, no infinities)
+ *           or LIGER_KV_INT8 (-127 .. 127).
+ *   scales  [n_blocks, Hkv, 2]  fp32, positive: a value is code * scale.
+ *   slot    block * block_size + offset: the place of one token.
+ *   block_table [B, table_width] int32: the blocks of each sequence in order; entries
+ *           behind its ceil(len / block_size) first ones are not read.
+ * block_size is 16, 32, 64 or 128, n_blocks * block_size and table_width * block_size fit
+ * 31 bits, and a call takes at most 8192 sequences (else LIGER_ERR_UNSUPPORTED).  One
+ * decode step is liger_kv_cache_assign, liger_kv_cache_append and liger_attn_cached
+ * on one stream; all three can be captured into a CUDA graph and replayed.
+ */
+typedef enum { LIGER_KV_E4M3 = 0, LIGER_KV_INT8 = 1 } liger_kv_dtype;
+
+/*
+ * Block tables and slot maps from request lengths, on the device.  Sequence s holds
+ * seq_lens[s] cached tokens.
+ *   new_lens[s] >= 0  as many tokens are to be added.  Blocks are taken from the front of
+ *           the free ring, for the sequences in order, and written behind the sequence's
+ *           blocks in its row of the table.  A sequence is served if its tokens fit its row
+ *           and the slot map and the free blocks last for it and all before it; else none
+ *           of its tokens gets a slot (-1) and its length stays (a later sequence that
+ *           needs no block is still served).
+ *   new_lens[s] < 0   the sequence ends: its blocks go behind the free ones (for the
+ *           next call), its length becomes 0.
+ * The new tokens stand packed, in the order of the sequences: sequence s has tokens
+ * cu_new[s] .. cu_new[s + 1] - 1, served or not.
+ *   new_lens, seq_lens [B]     int32 (in)  lengths are read as if in [0, table_width * block_size]
+ *   block_table  [B, table_width] int32 (in/out)
+ *   free_blocks  [n_blocks]    int32 (in/out) ring of free block numbers
+ *   free_span    [2]           int32 (in)  place of the first free block in the ring, and
+ *                their count.  Free blocks and blocks of sequences are n_blocks in all.
+ *   slot_map     [n_slots]     int32 (out, 16-byte aligned) slot of each new token; -1
+ *                behind the last one, for unserved tokens and where a table entry is no block
+ *   cu_new       [B + 1]       int32 (out)
+ *   seq_lens_out [B], free_span_out [2]  int32 (out)  the state after the call; may be
+ *                seq_lens and free_span themselves.
+ * A call on the same seq_lens and free_span (not overwritten) gives the same result again.
+ */
+liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_lens, int32_t* block_table,
+                                   int32_t* free_blocks, const int32_t* free_span, int32_t* slot_map, int32_t* cu_new,
+                                   int32_t* seq_lens_out, int32_t* free_span_out, int B, int table_width, int n_blocks,
+                                   int block_size, int n_slots, void* stream);
+
+/*
+ * Quantises keys and values into their slots.
+ *   k, v      [n_tokens, Hkv, d] dt (in)  tokens k_stride / v_stride elements apart (at
+ *             least Hkv * d, a multiple of 16 bytes), heads and elements contiguous
+ *   slot_map  [n_tokens] int32 (in)  a token whose slot is not in the cache (-1) is left out
+ *   cache, scales (in/out)
+ * The tokens that a call brings to one block have to be consecutive in it, with consecutive
+ * slots, as liger_kv_cache_assign gives them (no slot twice; a block belongs to one
+ * sequence).  For each of them together, per kv head, and for keys and values
+ * apart: with amax their largest finite magnitude, s = 2^e, e >= -64 the smallest with
+ * amax <= 448 * 2^e (e4m3) or 127 * 2^e (int8).  Tokens from offset 0 on give the block the scale s.
+ * Others raise it to s if it is smaller, and the older tokens of the block are requantised
+ * under the new scale.  Codes are x / scale to nearest, ties to even, saturated; NaN is
+ * kept (e4m3) or becomes 0 (int8).  Slots that get no token, and blocks that get none, are
+ * left as they are.
+ */
+liger_status liger_kv_cache_append(const void* k, const void* v, const int32_t* slot_map, void* cache, float* scales,
+                                   int n_tokens, int Hkv, int d, int n_blocks, int block_size, long long k_stride,
+                                   long long v_stride, liger_dtype dt, liger_kv_dtype kv_dt, void* stream);
+
+/*
+ * Softmax attention of the newest n_q tokens of each sequence over its cached tokens
+ * (themselves included: append them first).  With len = seq_lens[s], query i of n_q is
+ * token len - n_q + i and sees the cached tokens up to itself:
+ *   o_i = sum_{j <= len - n_q + i} softmax_j(q_i . k_j / sqrt(d)) v_j,  kv head h / (Hq/Hkv).
+ * A query that sees no token (len too short) gets zeros.  A table entry that is no block
+ * number stands for tokens that are not there.  Slots behind a sequence's last token may
+ * hold anything.
+ *   q    [B, n_q, Hq, d] dt (in)  tokens q_stride elements apart (at least Hq * d, a
+ *        multiple of 16 bytes), heads and elements contiguous
+ *   out  [B, n_q, Hq, d] dt (out)
+ *   seq_lens [B] int32 (in)  read as if in [0, table_width * block_size]
+ *   workspace  liger_attn_cached_workspace_size(d) bytes of device scratch (16-byte
+ *        aligned; contents on entry ignored, nothing kept in it between calls, so calls
+ *        in stream order may share it).
+ * Results do not depend on timing.  n_q is at most LIGER_CACHED_MAX_NEW.  Every internal
+ * wait is bounded; liger_attn_cached_status() reports whether any call on the current
+ * device gave up since the last query (synchronous read; call it after the stream has
+ * completed; it clears the report).
+ */
+#define LIGER_CACHED_MAX_NEW 16
+size_t liger_attn_cached_workspace_size(int d);
+liger_status liger_attn_cached(const void* q, const void* cache, const float* scales, const int32_t* block_table,
+                               const int32_t* seq_lens, void* out, int B, int n_q, int Hq, int Hkv, int d,
+                               int table_width, int n_blocks, int block_size, long long q_stride, liger_dtype dt,
+                               liger_kv_dtype kv_dt, void* workspace, size_t workspace_bytes, void* stream);
+liger_status liger_attn_cached_status(void);
+
 /* Message of the last failure on the calling thread ("" if none). */
 const char* liger_last_error(void);
 
