@@ -68,7 +68,7 @@ struct Args {
   void* out;                // [B, n_q, Hq, d]
   float* part_ml;           // [2 ctas][2][kMaxRows] references and sums of the parts
   float* part_o;            // [2 ctas][kMaxRows][d]
-  int4* split;              // [ctas] the unit that a CTA begins and does not end: (sequence, unit, last CTA, 1)
+  int4* split;              // [ctas] the unit that goes on behind a CTA's stretch: (sequence or -1, unit, first CTA, last CTA)
   uint32_t* err;
   uint64_t wait_ns;
   long qstride;
@@ -81,7 +81,7 @@ constexpr int kMaxRows = 16;           // query rows of a unit
 struct StageInfo {
   int seq, head, row0, tok0;           // kv head, first query row, first cached token
   int len, flags;                      // tokens of the sequence; kFirst | kLast | kBegins | kEnds
-  int pad0, pad1;
+  int tiles, pad;                      // tiles of the unit
   float ks[4], lv[4], iv[4];           // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
 };
 enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };   // the first, last tile of this CTA's stretch of the unit / of the unit itself
@@ -96,7 +96,7 @@ struct Smem {
   static constexpr uint32_t ML = kWarps * 8 * NT * 2 * 4;
   static constexpr int MAX_STAGES = 12;
   static constexpr uint32_t FIXED = RED + ML + MAX_STAGES * (sizeof(StageInfo) + 16) + 16 + 64;
-  static uint32_t bytes(int stages, int B) { return 1024 + stages * STAGE + FIXED + 4 * (B + 1); }
+  static uint32_t bytes(int stages, int B) { return 1024 + stages * STAGE + FIXED + 4 * (2 * B + 1); }
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -180,6 +180,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(part + 8);
   volatile uint32_t* never = abort_flag + 1;
   int* first = part + 16;                                             // [B + 1] 64-token tiles before each sequence
+  int* lens = first + a.B + 1;                                        // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -195,14 +196,14 @@ __global__ void __launch_bounds__(kThreads, 2)
   kvc::pdl_wait_previous();
 
   const int cap = a.width << a.lbs;
-  auto length = [&](int s) { const int n = a.lens[s]; return n < 0 ? 0 : (n > cap ? cap : n); };
   // tiles before each sequence: a block scan, each thread over consecutive sequences
   {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int s0 = tid * per, s1 = min(a.B, s0 + per);
     int sum = 0;
     for (int s = s0; s < s1; ++s) {
-      const int n = (length(s) + kTile - 1) / kTile;
+      const int len = min(max(a.lens[s], 0), cap), n = (int)(((long long)len + kTile - 1) / kTile);
+      lens[s] = len;
       first[s + 1] = n;
       sum += n;
     }
@@ -225,126 +226,144 @@ __global__ void __launch_bounds__(kThreads, 2)
   // as many CTAs as there are tiles, so that no stretch is empty (a unit's parts are those of consecutive CTAs)
   const int cta = blockIdx.x, n_cta = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
   const long long w0 = cta < n_cta ? stretch_begin(W, cta, n_cta) : W, w1 = cta < n_cta ? stretch_begin(W, cta + 1, n_cta) : W;
-  if (tid == 0) a.split[cta] = make_int4(0, 0, 0, 0);        // (the consumers' barriers order a later write behind this one)
+  if (tid == 0) a.split[cta] = make_int4(-1, 0, 0, 0);       // (the same thread writes it again)
   const WaitCtx wc{abort_flag, a.err, a.wait_ns};
 
+  const int bs = 1 << a.lbs, lbox = a.lbs < 6 ? a.lbs : 6, box = 1 << lbox;   // rows of keys, and of values, of one copy
+
   if (warp == kWarps) {   // ---------------- producer
-    const int bs = 1 << a.lbs;
-    const int lppt = a.lbs >= 6 ? 0 : 6 - a.lbs, ppt = 1 << lppt;       // blocks of a tile
-    const int box = bs < kTile ? bs : kTile;                            // rows of one copy
-    const int batch = 32 >> lppt;                                       // tiles looked up at once
-    struct Item { int seq, unit, tile, len, id; float ks, vs; bool live; };
-    const int in_tile = lane & (ppt - 1), lane_tile = lane >> lppt;
-    // the lane's entry of the batch of tiles that starts at w: everything but the scales
-    auto find = [&](long long w) {
-      Item it;
+    const int lppt = 6 - lbox;                       // 2^lppt blocks of a tile
+    const int batch = 32 >> lppt;                    // tiles looked up at once, a lane per block
+    const int in_tile = lane & ((1 << lppt) - 1), lane_tile = lane >> lppt;
+    struct Item { int seq, unit, tile, tiles, id; float ks, vs; };
+    // The lane's block of the batch that starts at w: its place in the line, then its number (`id`, as the table
+    // has it), then its scales.  Each step's load is used a batch later, so none is waited for but the first.
+    auto locate = [&](long long w, int lo) {
+      Item it{lo, 0, 0, 0, -1, 0.f, 1.f};
       w += lane_tile;
-      it.live = w < w1;
-      it.seq = it.unit = it.tile = it.len = 0;
-      it.id = -1;
-      it.ks = 0.f;
-      it.vs = 1.f;
-      if (it.live) {
-        const int f = (int)(w / units);
-        int lo = 0, hi = a.B;   // first[lo] <= f < first[hi]
-        while (hi - lo > 1) {
-          const int mid = (lo + hi) >> 1;
-          if (first[mid] <= f) lo = mid;
-          else hi = mid;
+      if (w < w1) {
+        if ((long long)first[lo + 1] * units <= w) {
+          int hi = a.B;   // first[lo] * units <= w < first[hi] * units
+          while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if ((long long)first[mid] * units <= w) lo = mid;
+            else hi = mid;
+          }
         }
-        const int n = first[lo + 1] - first[lo];
-        const int r = (int)(w - (long long)first[lo] * units);
+        const long long r = w - (long long)first[lo] * units;
         it.seq = lo;
-        it.unit = r / n;
-        it.tile = r - it.unit * n;
-        it.len = length(lo);
-        const int tok = it.tile * kTile + in_tile * box;
-        if (tok < it.len) {
-          const int id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
-          it.id = id < 0 || id >= a.n_blocks ? -1 : id;
-        }
+        it.tiles = first[lo + 1] - first[lo];
+        it.unit = r >> 32 ? (int)(r / it.tiles) : (int)((uint32_t)r / (uint32_t)it.tiles);
+        it.tile = (int)(r - (long long)it.unit * it.tiles);
+        const long long tok = (long long)it.tile * kTile + in_tile * box;
+        if (tok < lens[lo]) it.id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
       }
       return it;
     };
     auto fetch_scales = [&](Item& it) {
+      if (it.id < 0 || it.id >= a.n_blocks) it.id = -1;
       if (it.id >= 0) {
-        const float2 s = *reinterpret_cast<const float2*>(
-            a.scales + ((size_t)it.id * a.Hkv + it.unit / a.row_tiles) * 2);
+        const float2 s = *reinterpret_cast<const float2*>(a.scales + ((size_t)it.id * a.Hkv + it.unit / a.row_tiles) * 2);
         it.ks = s.x;
         it.vs = s.y;
       }
     };
-    Item cur = find(w0), next = find(w0 + batch);
-    int k = 0;   // tiles issued
+    Item cur = locate(w0, 0), next = locate(w0 + batch, cur.seq);
+    fetch_scales(cur);
+    int st = 0, issued = 0, turn = 0;   // the next stage, tiles issued (up to `stages`), uses of the stages
     bool ok = true;
     for (long long wb = w0; wb < w1 && ok; wb += batch) {
-      if (wb == w0) fetch_scales(cur);   // (used only behind the first tile's copies)
-      fetch_scales(next);
-      const Item later = find(wb + 2 * batch);
       const int n_here = (int)(w1 - wb < batch ? w1 - wb : batch);
-      for (int t = 0; t < n_here && ok; ++t, ++k) {
-        const int st = k % stages, use = k / stages;
-        if (use > 0) ok = warp_all(mbar_wait(&empty[st], (use - 1) & 1, wc, wsite(1, st, k)));
-        if (!ok) break;
+      const long long w = wb + lane_tile;
+      const int head = cur.unit / a.row_tiles, row0 = (cur.unit - head * a.row_tiles) * kMaxRows;
+      const bool opens = cur.tile == 0 || w == w0, ends = cur.tile == cur.tiles - 1;
+      const int flags = (opens ? kFirst : 0) | (ends || w == w1 - 1 ? kLast : 0) | (cur.tile == 0 ? kBegins : 0) | (ends ? kEnds : 0);
+      const uint32_t live = __ballot_sync(0xffffffffu, cur.id >= 0), opening = __ballot_sync(0xffffffffu, opens);
+      // a tile's copies: keys and values of each block in one, and the query rows where a unit starts
+      auto issue = [&](int t, int at) {
         const int owner = t << lppt;
-        const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), unit = __shfl_sync(0xffffffffu, cur.unit, owner);
-        const int tile = __shfl_sync(0xffffffffu, cur.tile, owner), len = __shfl_sync(0xffffffffu, cur.len, owner);
-        const int head = unit / a.row_tiles, row0 = (unit - head * a.row_tiles) * kMaxRows;
-        const bool mine = lane_tile == t && cur.id >= 0;
-        const uint32_t live = __ballot_sync(0xffffffffu, mine);
-        const bool opens = tile == 0 || (wb == w0 && t == 0);
-        const int n_rows = min(kRows, a.rows - row0);
-        char* sk = smem + st * S::STAGE;
-        if (lane == 0)
-          mbar_expect_tx(&full[st], __popc(live) * 2 * box * D + (opens ? n_rows * D * (uint32_t)sizeof(Tin) : 0u));
+        const bool open = (opening >> owner) & 1u;
+        const int u_row0 = __shfl_sync(0xffffffffu, row0, owner);
+        const int n_rows = open ? min(kRows, a.rows - u_row0) : 0;
+        const int blocks = __popc((live >> owner) & ((1u << (1 << lppt)) - 1u));
+        if (lane == 0) mbar_expect_tx(&full[at], (uint32_t)(blocks * 2 * box * D + n_rows * D * (int)sizeof(Tin)));
         __syncwarp();
-        if (mine) {
-          const int z = cur.id * a.Hkv + head;
-          const int y = (tile * kTile) & (bs - 1);
-          tma_load_3d(sk + in_tile * box * D, &tm, &full[st], 0, y, z);
-          tma_load_3d(sk + S::KV + in_tile * box * D, &tm, &full[st], 0, bs + y, z);
-        }
-        if (opens && lane < n_rows) {   // the unit's query rows: (token, head) pairs
-          const int row = row0 + lane, i = row / a.G, g = row - i * a.G;
-          bulk_load(sk + 2 * S::KV + lane * D * sizeof(Tin),
-                    static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(head * a.G + g) * D,
-                    D * sizeof(Tin), &full[st]);
-        }
-        StageInfo& si = info[st];
-        if (lane_tile == t) {   // the scales of this lane's block, for each 16 tokens of it
-          const float lv = log2f(cur.vs), iv = 1.f / cur.vs;
-          for (int e = 0; e < 4 >> lppt; ++e) {
-            const int slot = in_tile * (4 >> lppt) + e;
-            si.ks[slot] = cur.id >= 0 ? cur.ks : 0.f;
-            si.lv[slot] = lv;
-            si.iv[slot] = iv;
+        char* dst = smem + at * S::STAGE;
+        if (lane_tile == t && cur.id >= 0)
+          tma_load_4d(dst + in_tile * 2 * box * D, &tm, &full[at], 0, (int)(((long long)cur.tile * kTile) & (bs - 1)), 0,
+                      cur.id * a.Hkv + head);
+        if (open) {   // (token, head) pairs
+          const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), u_head = __shfl_sync(0xffffffffu, head, owner);
+          if (lane < n_rows) {
+            const int row = u_row0 + lane, i = row / a.G, g = row - i * a.G;
+            bulk_load(dst + 2 * S::KV + lane * D * sizeof(Tin),
+                      static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(u_head * a.G + g) * D,
+                      D * sizeof(Tin), &full[at]);
           }
         }
-        if (lane == 0) {
-          const int n = first[seq + 1] - first[seq];
-          si.seq = seq;
-          si.head = head;
-          si.row0 = row0;
-          si.tok0 = tile * kTile;
-          si.len = len;
-          const bool ends = tile == n - 1;
-          si.flags = (opens ? kFirst : 0) | (ends || wb + t == w1 - 1 ? kLast : 0) | (tile == 0 ? kBegins : 0) |
-                     (ends ? kEnds : 0);
+      };
+      float ks, lv, iv;   // of the lane's block
+      // a tile's description for the consumers; the scales once for each 16 tokens
+      auto publish = [&](int t, int at) {
+        StageInfo& si = info[at];
+        if (lane_tile == t) {
+          if (lppt == 0) {
+            *reinterpret_cast<float4*>(si.ks) = make_float4(ks, ks, ks, ks);
+            *reinterpret_cast<float4*>(si.lv) = make_float4(lv, lv, lv, lv);
+            *reinterpret_cast<float4*>(si.iv) = make_float4(iv, iv, iv, iv);
+          } else {
+            for (int e = 0; e < 4 >> lppt; ++e) {
+              const int slot = in_tile * (4 >> lppt) + e;
+              si.ks[slot] = ks;
+              si.lv[slot] = lv;
+              si.iv[slot] = iv;
+            }
+          }
+          if (in_tile == 0) {
+            *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, head, row0, cur.tile * kTile);
+            *reinterpret_cast<int4*>(&si.len) = make_int4(lens[cur.seq], flags, cur.tiles, 0);
+          }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[st]);
+        if (lane == 0) mbar_arrive(&full[at]);
+      };
+      int t = 0;
+      if (wb == w0)   // the first tiles' copies do not wait for their scales
+        for (; t < n_here && t < stages; ++t) issue(t, t);
+      ks = cur.id >= 0 ? cur.ks : 0.f;
+      lv = log2f(cur.vs);
+      iv = 1.f / cur.vs;
+      for (int i = 0; i < t; ++i) publish(i, i);
+      if (wb == w0) {
+        issued = t;
+        st = t == stages ? 0 : t;
+        turn = t == stages ? 1 : 0;
+      }
+      fetch_scales(next);
+      const Item later = locate(wb + 2 * batch, next.seq);
+      for (; t < n_here; ++t) {
+        if (turn > 0) ok = warp_all(mbar_wait(&empty[st], (turn - 1) & 1, wc, wsite(1, st, turn)));
+        if (!ok) break;
+        issue(t, st);
+        publish(t, st);
+        issued = min(issued + 1, stages);
+        if (++st == stages) { st = 0; ++turn; }
       }
       cur = next;
       next = later;
     }
     // never leave with copies in flight
     const WaitCtx dw{never, nullptr, a.wait_ns};
-    for (int i = k > stages ? k - stages : 0; i < k; ++i) mbar_wait(&full[i % stages], (i / stages) & 1, dw);
+    for (int i = 0; i < issued; ++i) {
+      if (--st < 0) { st = stages - 1; --turn; }
+      mbar_wait(&full[st], turn & 1, dw);
+    }
     return;
   }
 
   // ---------------- consumers: warp w takes tokens 16 w .. 16 w + 15 of each tile
   const int g = lane >> 2, t4 = lane & 3;
+  const int krow = ((16 * warp) >> lbox) * 2 * box + ((16 * warp) & (box - 1));   // of the warp's tokens in a stage
   // sequences without tokens: zero rows
   for (int s = cta; s < a.B; s += gridDim.x)
     if (first[s + 1] == first[s]) {
@@ -362,24 +381,22 @@ __global__ void __launch_bounds__(kThreads, 2)
   int row0 = 0;
   bool begins = false;                  // the CTA's stretch of the unit starts with its first tile
   uint32_t joins = 0;
-  // all consumer warps meet (bounded, as every wait: a warp that gave up frees the others)
-  auto meet = [&](int b, int k) {
+  // barrier `b` of all consumer warps (bounded, as every wait: a warp that gave up frees the others)
+  auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(&joined[b]);
-    return warp_all(mbar_wait(&joined[b], joins & 1, wc, wsite(3, b, k)));
   };
+  auto wait_for = [&](int b, uint32_t use, int k) { return warp_all(mbar_wait(&joined[b], use & 1, wc, wsite(3, b, k))); };
   const int n_tiles = (int)(w1 - w0);
-  for (int k = 0; k < n_tiles; ++k) {
-    const int st = k % stages;
-    if (!warp_all(mbar_wait(&full[st], (k / stages) & 1, wc, wsite(2, st, k)))) return;
+  for (int k = 0, st = 0, phase = 0; k < n_tiles; ++k) {
+    if (!warp_all(mbar_wait(&full[st], phase, wc, wsite(2, st, k)))) return;
     const StageInfo& si = info[st];
     const char* sk = smem + st * S::STAGE;
-    const char* sv = sk + S::KV;
     const int flags = si.flags, len = si.len, tok = si.tok0 + 16 * warp;
     if (flags & kFirst) {
       row0 = si.row0;
       begins = (flags & kBegins) != 0;
-      const char* sq = sv + S::KV;
+      const char* sq = sk + 2 * S::KV;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         // row g of this eight: the thread's d are those whose key bytes it reads (16-byte column c = word j / 4)
@@ -437,7 +454,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     const float ks = si.ks[warp], lv = si.lv[warp], iv = si.iv[warp];
     if (tok < len && ks != 0.f) {
       // keys: rows g and g + 8 of the warp's 16 tokens
-      const int r0 = 16 * warp + token_of(g);
+      const int r0 = krow + token_of(g);
       uint32_t kw[2][KS];
 #pragma unroll
       for (int r = 0; r < 2; ++r)
@@ -446,19 +463,6 @@ __global__ void __launch_bounds__(kThreads, 2)
           const uint4 u = *reinterpret_cast<const uint4*>(sk + swz<D>(r0 + 8 * r, (D == 128 ? 2 * t4 + c : t4) * 16));
           kw[r][4 * c] = u.x; kw[r][4 * c + 1] = u.y; kw[r][4 * c + 2] = u.z; kw[r][4 * c + 3] = u.w;
         }
-      // values: this thread's four tokens, D / 8 bytes at column g
-      uint32_t vw[4][D / 32];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = 16 * warp + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
-        if (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sv + swz<D>(row, g * 16));
-          vw[r][0] = u.x; vw[r][1] = u.y; vw[r][D / 32 - 2] = u.z; vw[r][D / 32 - 1] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sv + swz<D>(row, g * 8));
-          vw[r][0] = u.x; vw[r][1] = u.y;
-        }
-      }
       float s[NT][4];
 #pragma unroll
       for (int n = 0; n < NT; ++n)
@@ -517,6 +521,19 @@ __global__ void __launch_bounds__(kThreads, 2)
         sum[n][0] = fmaf(p[n][0] + p[n][2], iv, sum[n][0]);
         sum[n][1] = fmaf(p[n][1] + p[n][3], iv, sum[n][1]);
       }
+      // values: this thread's four tokens, D / 8 bytes at column g
+      uint32_t vw[4][D / 32];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) {
+        const int row = krow + box + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
+        if (D == 128) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sk + swz<D>(row, g * 16));
+          vw[r][0] = u.x; vw[r][1] = u.y; vw[r][D / 32 - 2] = u.z; vw[r][D / 32 - 1] = u.w;
+        } else {
+          const uint2 u = *reinterpret_cast<const uint2*>(sk + swz<D>(row, g * 8));
+          vw[r][0] = u.x; vw[r][1] = u.y;
+        }
+      }
       // O^T += V^T P^T.  At the sequence's end (edge) there is one pass for each new token, over the value
       // codes that it sees, and only its rows take the sums: with weights of zero alone, a NaN code behind
       // a row's last visible token would reach it.
@@ -574,13 +591,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int sees = max(len - a.n_q + 1, tok + 1); sees <= len; ++sees) weigh(std::true_type{}, sees);
       }
     }
-    const int seq = si.seq, head = si.head, tile = si.tok0 / kTile;
+    const int seq = si.seq, head = si.head, tile = si.tok0 / kTile, tiles = si.tiles;
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
+    if (++st == stages) { st = 0; phase ^= 1; }
 
     if (flags & kLast) {
       // join the four warps' parts of this stretch of the unit
       const int n_rows = min(kRows, a.rows - row0);
+      if (joins > 0 && !wait_for(1, joins - 1, k)) return;   // the last unit's parts have been read
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -602,7 +621,8 @@ __global__ void __launch_bounds__(kThreads, 2)
                   make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
           }
         }
-      if (!meet(0, k)) return;
+      arrive(0);
+      if (!wait_for(0, joins, k)) return;
       const bool whole = begins && (flags & kEnds);
       const bool carries_on = !begins;              // part of a unit that an earlier CTA began
       const int slot = 2 * cta + (carries_on ? 0 : 1);
@@ -637,90 +657,77 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
       }
-      if (!whole && !carries_on && tid == 0) {   // the unit goes on in later stretches
-        const long long last = w0 + k + (first[seq + 1] - first[seq]) - 1 - tile;   // its last tile
-        a.split[cta] = make_int4(seq, head * a.row_tiles + row0 / kMaxRows, stretch_of(W, last, n_cta), 1);
+      if (!(flags & kEnds) && tid == 0) {   // the unit goes on in later stretches
+        const long long w = w0 + k - tile;  // its first tile
+        a.split[cta] = make_int4(seq, head * a.row_tiles + row0 / kMaxRows, stretch_of(W, w, n_cta), stretch_of(W, w + tiles - 1, n_cta));
       }
-      if (!meet(1, k)) return;   // the buffers are free again
+      arrive(1);
       ++joins;
     }
   }
 }
 
-// Joins a unit that one CTA of cached_attn_kernel began and did not end: its parts stand in the
-// begin slot of that CTA and in the continue slots of the next ones.  One CTA per CTA of the
-// first kernel; the parts are added in their order.
+// Joins the units that lie in several stretches: the parts stand in the begin slot of the unit's first CTA and in the
+// continue slots of the others, and are added in a fixed order.  Each CTA whose stretch a unit goes on behind (all of the
+// unit's but the last) takes a share of the unit's output, 16 bytes a thread; up to kJoinLanes threads share the parts.
 constexpr int kJoinThreads = 256;
+constexpr int kJoinLanes = 16;
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
-  extern __shared__ float sh[];
+  __shared__ float4 s_x[kJoinThreads];
+  __shared__ float2 s_ml[kJoinThreads];
   const int tid = threadIdx.x;
   kvc::pdl_launch_next();
   kvc::pdl_wait_previous();
-  const int c0 = blockIdx.x;
-  const int4 u = a.split[c0];
-  if (!u.w) return;
+  const int4 u = a.split[blockIdx.x];
+  if (u.x < 0) return;
   const int head = u.y / a.row_tiles, row0 = (u.y - head * a.row_tiles) * kMaxRows;
-  const int n_rows = min(kMaxRows, a.rows - row0), parts = min(u.z, (int)gridDim.x - 1) - c0 + 1;
-  auto slot_of = [&](int p) { return p == 0 ? 2 * c0 + 1 : 2 * (c0 + p); };
-  float* wgt = sh;                            // [parts][kMaxRows] 2^(m_part - m) / l
-  float4* acc = reinterpret_cast<float4*>(sh + (size_t)gridDim.x * kMaxRows);   // [kJoinThreads]
-  // weights: eight lanes per row
-  {
-    constexpr int kLanes = 8;
-    const int r = tid / kLanes, e = tid % kLanes;
-    const bool in = r < n_rows;
+  const int c0 = u.z, parts = u.w - c0 + 1;
+  const int vecs = min(kMaxRows, a.rows - row0) * (D / 4);
+  const int share = (vecs + parts - 2) / (parts - 1);              // of each of the unit's CTAs but the last
+  const int v0 = ((int)blockIdx.x - c0) * share, v1 = min(vecs, v0 + share);
+  const int lanes = max(1, min(min(kJoinLanes, parts), kJoinThreads / share)), step = min(share, kJoinThreads);
+  const int e = tid / step;
+  for (int vb = v0; vb < v1; vb += step) {
+    const int v = vb + tid % step, r = v / (D / 4), c = v % (D / 4);
+    const bool in = v < v1 && e < lanes;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = kNoRef, l = 0.f;
     if (in)
-      for (int p = e; p < parts; p += kLanes) m = fmaxf(m, a.part_ml[(size_t)slot_of(p) * 2 * kMaxRows + r]);
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (in)
-      for (int p = e; p < parts; p += kLanes) {
-        const float* ml = a.part_ml + (size_t)slot_of(p) * 2 * kMaxRows + r;
-        const float f = ex2(ml[0] - m);
-        wgt[p * kMaxRows + r] = f;
-        l = fmaf(f, ml[kMaxRows], l);
-      }
-#pragma unroll
-    for (int o = 1; o < kLanes; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    const float il = l == 0.f ? 0.f : 1.f / l;
-    if (in)
-      for (int p = e; p < parts; p += kLanes) wgt[p * kMaxRows + r] *= il;
-  }
-  __syncthreads();
-  // the sum: `lanes` threads of a float4 of the output each take every lanes-th part
-  const int vecs = n_rows * (D / 4);
-  const int lanes = vecs >= kJoinThreads ? 1 : kJoinThreads / vecs;
-  for (int v0 = 0; v0 < vecs; v0 += kJoinThreads) {
-    const int v = v0 + tid % (lanes > 1 ? vecs : kJoinThreads), e = lanes > 1 ? tid / vecs : 0;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    const int r = v / (D / 4), c = v % (D / 4);
-    const bool in = v < vecs && e < lanes;
-    if (in)
-#pragma unroll 8
+#pragma unroll 4
       for (int p = e; p < parts; p += lanes) {
-        const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((size_t)slot_of(p) * kMaxRows + r) * D + 4 * c);
-        const float f = wgt[p * kMaxRows + r];
-        x.x = fmaf(f, y.x, x.x); x.y = fmaf(f, y.y, x.y);
-        x.z = fmaf(f, y.z, x.z); x.w = fmaf(f, y.w, x.w);
+        const int slot = p == 0 ? 2 * c0 + 1 : 2 * (c0 + p);
+        const float* ml = a.part_ml + (size_t)slot * 2 * kMaxRows + r;
+        const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((size_t)slot * kMaxRows + r) * D + 4 * c);
+        const float pm = ml[0], pl = ml[kMaxRows], top = fmaxf(m, pm), f = ex2(m - top), g = ex2(pm - top);
+        m = top;
+        l = l * f + pl * g;
+        x.x = x.x * f + y.x * g; x.y = x.y * f + y.y * g;
+        x.z = x.z * f + y.z * g; x.w = x.w * f + y.w * g;
       }
     if (lanes > 1) {
-      acc[tid] = x;
+      s_x[tid] = x;
+      s_ml[tid] = make_float2(m, l);
       __syncthreads();
       if (in && e == 0)
         for (int q = 1; q < lanes; ++q) {
-          const float4 y = acc[q * vecs + v];
-          x.x += y.x; x.y += y.y; x.z += y.z; x.w += y.w;
+          const float4 y = s_x[q * step + tid];
+          const float2 o = s_ml[q * step + tid];
+          const float top = fmaxf(m, o.x), f = ex2(m - top), g = ex2(o.x - top);
+          m = top;
+          l = l * f + o.y * g;
+          x.x = x.x * f + y.x * g; x.y = x.y * f + y.y * g;
+          x.z = x.z * f + y.z * g; x.w = x.w * f + y.w * g;
         }
     }
     if (in && e == 0) {
+      const float il = l == 0.f ? 0.f : 1.f / l;
       const int row = row0 + r, i = row / a.G, h = head * a.G + row - i * a.G;
       Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.x * a.n_q + i) * a.Hq + h) * D + 4 * c;
       if (sizeof(Tin) == 2)
-        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x.x, x.y), pack_bf16(x.z, x.w));
+        *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x.x * il, x.y * il), pack_bf16(x.z * il, x.w * il));
       else
-        *reinterpret_cast<float4*>(dst) = x;
+        *reinterpret_cast<float4*>(dst) = make_float4(x.x * il, x.y * il, x.z * il, x.w * il);
     }
   }
 }

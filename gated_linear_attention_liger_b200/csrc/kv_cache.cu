@@ -185,13 +185,7 @@ liger_status launch_attn(const CUtensorMap& tm, const liger::ca::Args& a, int ct
   e = launch(kern, dim3((unsigned)ctas), liger::ca::kThreads, (size_t)smem, s, tm, a, stages);
   if (e != cudaSuccess) return cuda_fail(e, "cached attention launch");
   liger::mark_dominant_stop(s);
-  const size_t jsm = (size_t)ctas * liger::ca::kMaxRows * 4 + liger::ca::kJoinThreads * 16;
-  auto join = liger::ca::join_kernel<Tin, D>;
-  if (jsm > 48 * 1024) {
-    e = cudaFuncSetAttribute(join, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)jsm);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cached attention join)");
-  }
-  e = launch(join, dim3((unsigned)ctas), liger::ca::kJoinThreads, jsm, s, a);
+  e = launch(liger::ca::join_kernel<Tin, D>, dim3((unsigned)ctas), liger::ca::kJoinThreads, 0, s, a);
   if (e != cudaSuccess) return cuda_fail(e, "cached attention join launch");
   return LIGER_OK;
 }
@@ -306,14 +300,14 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   if (!workspace || workspace_bytes < L.total)
     return fail(LIGER_ERR_INVALID_ARG, "workspace too small: need %zu bytes, got %zu", L.total, workspace_bytes);
 
-  // the cache as (d, keys then values of a block, (block, kv head)) bytes; a copy brings up to 64 rows
+  // the cache as (d, tokens of a block, keys then values, (block, kv head)) bytes; a copy brings the keys and values of up to 64 tokens
   CUtensorMap tm;
   const auto enc = liger::tensor_map_encoder();
-  const cuuint64_t dims[3] = {(cuuint64_t)d, (cuuint64_t)2 * block_size, (cuuint64_t)n_blocks * Hkv};
-  const cuuint64_t strides[2] = {(cuuint64_t)d, (cuuint64_t)2 * block_size * d};
-  const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)(block_size < liger::ca::kTile ? block_size : liger::ca::kTile), 1};
-  const cuuint32_t es[3] = {1, 1, 1};
-  if (!enc || enc(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(cache), dims, strides, box, es,
+  const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)block_size, 2, (cuuint64_t)n_blocks * Hkv};
+  const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)block_size * d, (cuuint64_t)2 * block_size * d};
+  const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)(block_size < liger::ca::kTile ? block_size : liger::ca::kTile), 2, 1};
+  const cuuint32_t es[4] = {1, 1, 1, 1};
+  if (!enc || enc(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
     return fail(LIGER_ERR_CUDA, "cuTensorMapEncodeTiled failed for the cache");
