@@ -53,9 +53,8 @@ using kvc::KvType;
 using kvc::kE4m3;
 using kvc::kInt8;
 
-constexpr int kTile = 64;              // cached tokens of a stage
-constexpr int kWarps = 4;              // consumer warps; 16 tokens of a tile each
-constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kWarps = 4;              // consumer warps
+constexpr int kThreads = 32 * (kWarps + 2);   // and the producer's and the output's warp
 constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
 constexpr float kRefBelow = 7.f;       // the reference is set this far below the maximum,
 constexpr float kRaiseAt = 15.f;       // and raised when a score exceeds it by this much
@@ -82,21 +81,32 @@ struct StageInfo {
   int seq, head, row0, tok0;           // kv head, first query row, first cached token
   int len, flags;                      // tokens of the sequence; kFirst | kLast | kBegins | kEnds
   int tiles, pad;                      // tiles of the unit
-  float ks[4], lv[4], iv[4];           // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
+  float ks[8], lv[8], iv[8];           // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
 };
 enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };   // the first, last tile of this CTA's stretch of the unit / of the unit itself
+
+// Cached tokens of a tile: 16 KB of keys and values, whatever d, since a tile costs the producer and each consumer warp
+// about 1000 cycles besides its bytes.
+constexpr int tile_tokens(int d) { return 8192 / d; }
+
+// What the consumer warps tell the output's warp about the unit that they have just ended.
+struct UnitInfo {
+  int seq, head, row0, flags;
+  int tile, tiles, k, pad;             // the last tile's number in the unit, the unit's tiles, the tile's number in the stretch
+};
 
 // Shared memory.  NT: query rows in eights (1 or 2).
 template <typename Tin, int D, int NT>
 struct Smem {
-  static constexpr uint32_t KV = kTile * D;                       // keys (or values) of a tile
+  static constexpr uint32_t KV = 16384;                           // keys and values of a tile
   static constexpr uint32_t Q = 8 * NT * D * sizeof(Tin);
-  static constexpr uint32_t STAGE = 2 * KV + Q;                   // a multiple of 1024
-  static constexpr uint32_t RED = kWarps * 8 * NT * D * 4;        // partial outputs of the warps
-  static constexpr uint32_t ML = kWarps * 8 * NT * 2 * 4;
+  static constexpr uint32_t STAGE = KV + Q;                       // a multiple of 1024
   static constexpr int MAX_STAGES = 12;
-  static constexpr uint32_t FIXED = RED + ML + MAX_STAGES * (sizeof(StageInfo) + 16) + 16 + 64;
-  static uint32_t bytes(int stages, int B) { return 1024 + stages * STAGE + FIXED + 4 * (2 * B + 1); }
+  static constexpr uint32_t FIXED = MAX_STAGES * (sizeof(StageInfo) + 16) + sizeof(UnitInfo) + 16 + 64;
+  static __host__ __device__ int part_rows(int rows) { return rows < 8 * NT ? rows : 8 * NT; }
+  // the four warps' parts of a unit: sums, then references and sums of weights
+  static __host__ __device__ uint32_t red(int rows) { return kWarps * part_rows(rows) * (D * 4 + 8); }
+  static uint32_t bytes(int stages, int rows, int B) { return 1024 + stages * STAGE + FIXED + (red(rows) + 15) / 16 * 16 + 4 * (2 * B + 1); }
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -166,27 +176,29 @@ __global__ void __launch_bounds__(kThreads, 2)
     cached_attn_kernel(const __grid_constant__ CUtensorMap tm, Args a, int stages) {
   using S = Smem<Tin, D, NT>;
   constexpr bool kSplit = sizeof(Tin) == 4;                 // fp32: two fp16 terms of q and of p
-  constexpr int kRows = 8 * NT;
+  constexpr int kRows = 8 * NT, kTile = tile_tokens(D);
   extern __shared__ __align__(1024) char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  char* fixed = smem + stages * S::STAGE;
-  float* red = reinterpret_cast<float*>(fixed);
-  float* red_ml = reinterpret_cast<float*>(fixed + S::RED);
-  StageInfo* info = reinterpret_cast<StageInfo*>(fixed + S::RED + S::ML);
-  uint64_t* full = reinterpret_cast<uint64_t*>(info + S::MAX_STAGES);
+  StageInfo* info = reinterpret_cast<StageInfo*>(smem + stages * S::STAGE);
+  UnitInfo* unit_info = reinterpret_cast<UnitInfo*>(info + S::MAX_STAGES);
+  uint64_t* full = reinterpret_cast<uint64_t*>(unit_info + 1);
   uint64_t* empty = full + S::MAX_STAGES;
-  uint64_t* joined = empty + S::MAX_STAGES;                           // [2] the warps' parts written / read
-  int* part = reinterpret_cast<int*>(joined + 2);                     // [5] warp sums of the scan
+  uint64_t* parts_full = empty + S::MAX_STAGES;                       // the warps' parts are written
+  uint64_t* parts_empty = parts_full + 1;                             // and read
+  int* part = reinterpret_cast<int*>(parts_empty + 1);                // [6] warp sums of the scan
   volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(part + 8);
   volatile uint32_t* never = abort_flag + 1;
-  int* first = part + 16;                                             // [B + 1] 64-token tiles before each sequence
+  const int part_rows = S::part_rows(a.rows);
+  float* red = reinterpret_cast<float*>(part + 16);                   // [kWarps][part_rows][D]
+  float* red_ml = red + kWarps * part_rows * D;                       // [kWarps][part_rows][2]
+  int* first = reinterpret_cast<int*>(part + 16) + (S::red(a.rows) + 15) / 16 * 4;   // [B + 1] tiles before each sequence
   int* lens = first + a.B + 1;                                        // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
     for (int i = 0; i < stages; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], kWarps); }
-    mbar_init(&joined[0], kWarps);
-    mbar_init(&joined[1], kWarps);
+    mbar_init(parts_full, kWarps);
+    mbar_init(parts_empty, 1);
     *abort_flag = 0u;
     *never = 0u;
     fence_mbar_init();
@@ -226,20 +238,19 @@ __global__ void __launch_bounds__(kThreads, 2)
   // as many CTAs as there are tiles, so that no stretch is empty (a unit's parts are those of consecutive CTAs)
   const int cta = blockIdx.x, n_cta = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
   const long long w0 = cta < n_cta ? stretch_begin(W, cta, n_cta) : W, w1 = cta < n_cta ? stretch_begin(W, cta + 1, n_cta) : W;
-  if (tid == 0) a.split[cta] = make_int4(-1, 0, 0, 0);       // (the same thread writes it again)
   const WaitCtx wc{abort_flag, a.err, a.wait_ns};
 
-  const int bs = 1 << a.lbs, lbox = a.lbs < 6 ? a.lbs : 6, box = 1 << lbox;   // rows of keys, and of values, of one copy
+  const int bs = 1 << a.lbs, kLog = D == 128 ? 6 : 7, lbox = a.lbs < kLog ? a.lbs : kLog, box = 1 << lbox;   // rows of keys, and of values, of one copy
 
   if (warp == kWarps) {   // ---------------- producer
-    const int lppt = 6 - lbox;                       // 2^lppt blocks of a tile
+    const int lppt = kLog - lbox;                       // 2^lppt blocks of a tile
     const int batch = 32 >> lppt;                    // tiles looked up at once, a lane per block
     const int in_tile = lane & ((1 << lppt) - 1), lane_tile = lane >> lppt;
-    struct Item { int seq, unit, tile, tiles, id; float ks, vs; };
+    struct Item { int seq, head, row0, tile, tiles, id; float ks, vs; };
     // The lane's block of the batch that starts at w: its place in the line, then its number (`id`, as the table
     // has it), then its scales.  Each step's load is used a batch later, so none is waited for but the first.
     auto locate = [&](long long w, int lo) {
-      Item it{lo, 0, 0, 0, -1, 0.f, 1.f};
+      Item it{lo, 0, 0, 0, 0, -1, 0.f, 1.f};
       w += lane_tile;
       if (w < w1) {
         if ((long long)first[lo + 1] * units <= w) {
@@ -253,8 +264,13 @@ __global__ void __launch_bounds__(kThreads, 2)
         const long long r = w - (long long)first[lo] * units;
         it.seq = lo;
         it.tiles = first[lo + 1] - first[lo];
-        it.unit = r >> 32 ? (int)(r / it.tiles) : (int)((uint32_t)r / (uint32_t)it.tiles);
-        it.tile = (int)(r - (long long)it.unit * it.tiles);
+        const int unit = r >> 32 ? (int)(r / it.tiles) : (int)((uint32_t)r / (uint32_t)it.tiles);
+        it.tile = (int)(r - (long long)unit * it.tiles);
+        it.head = unit;
+        if (a.row_tiles > 1) {
+          it.head = unit / a.row_tiles;
+          it.row0 = (unit - it.head * a.row_tiles) * kMaxRows;
+        }
         const long long tok = (long long)it.tile * kTile + in_tile * box;
         if (tok < lens[lo]) it.id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
       }
@@ -263,7 +279,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     auto fetch_scales = [&](Item& it) {
       if (it.id < 0 || it.id >= a.n_blocks) it.id = -1;
       if (it.id >= 0) {
-        const float2 s = *reinterpret_cast<const float2*>(a.scales + ((size_t)it.id * a.Hkv + it.unit / a.row_tiles) * 2);
+        const float2 s = *reinterpret_cast<const float2*>(a.scales + ((size_t)it.id * a.Hkv + it.head) * 2);
         it.ks = s.x;
         it.vs = s.y;
       }
@@ -275,31 +291,28 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (long long wb = w0; wb < w1 && ok; wb += batch) {
       const int n_here = (int)(w1 - wb < batch ? w1 - wb : batch);
       const long long w = wb + lane_tile;
-      const int head = cur.unit / a.row_tiles, row0 = (cur.unit - head * a.row_tiles) * kMaxRows;
       const bool opens = cur.tile == 0 || w == w0, ends = cur.tile == cur.tiles - 1;
       const int flags = (opens ? kFirst : 0) | (ends || w == w1 - 1 ? kLast : 0) | (cur.tile == 0 ? kBegins : 0) | (ends ? kEnds : 0);
       const uint32_t live = __ballot_sync(0xffffffffu, cur.id >= 0), opening = __ballot_sync(0xffffffffu, opens);
+      const uint32_t blocks = (live >> (lane & ~((1 << lppt) - 1))) & ((1u << (1 << lppt)) - 1u);   // of the lane's tile
+      const uint32_t bytes = __popc(blocks) * 2 * box * D + (opens ? min(kRows, a.rows - cur.row0) * D * (int)sizeof(Tin) : 0);
       // a tile's copies: keys and values of each block in one, and the query rows where a unit starts
       auto issue = [&](int t, int at) {
-        const int owner = t << lppt;
-        const bool open = (opening >> owner) & 1u;
-        const int u_row0 = __shfl_sync(0xffffffffu, row0, owner);
-        const int n_rows = open ? min(kRows, a.rows - u_row0) : 0;
-        const int blocks = __popc((live >> owner) & ((1u << (1 << lppt)) - 1u));
-        if (lane == 0) mbar_expect_tx(&full[at], (uint32_t)(blocks * 2 * box * D + n_rows * D * (int)sizeof(Tin)));
+        if (lane_tile == t && in_tile == 0) mbar_expect_tx(&full[at], bytes);
         __syncwarp();
         char* dst = smem + at * S::STAGE;
         if (lane_tile == t && cur.id >= 0)
           tma_load_4d(dst + in_tile * 2 * box * D, &tm, &full[at], 0, (int)(((long long)cur.tile * kTile) & (bs - 1)), 0,
-                      cur.id * a.Hkv + head);
-        if (open) {   // (token, head) pairs
-          const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), u_head = __shfl_sync(0xffffffffu, head, owner);
-          if (lane < n_rows) {
-            const int row = u_row0 + lane, i = row / a.G, g = row - i * a.G;
-            bulk_load(dst + 2 * S::KV + lane * D * sizeof(Tin),
-                      static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(u_head * a.G + g) * D,
-                      D * sizeof(Tin), &full[at]);
-          }
+                      cur.id * a.Hkv + cur.head);
+        const int owner = t << lppt;
+        if ((opening >> owner) & 1u) {   // rows are (token, head) pairs: one copy for each token's heads
+          const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), head = __shfl_sync(0xffffffffu, cur.head, owner);
+          const int r0 = __shfl_sync(0xffffffffu, cur.row0, owner), r1 = min(r0 + kRows, a.rows);
+          const int i = r0 / a.G + lane, lo = max(r0, i * a.G), hi = min(r1, (i + 1) * a.G);
+          if (lo < hi)
+            bulk_load(dst + S::KV + (lo - r0) * D * sizeof(Tin),
+                      static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(head * a.G + lo - i * a.G) * D,
+                      (hi - lo) * D * sizeof(Tin), &full[at]);
         }
       };
       float ks, lv, iv;   // of the lane's block
@@ -307,20 +320,14 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto publish = [&](int t, int at) {
         StageInfo& si = info[at];
         if (lane_tile == t) {
-          if (lppt == 0) {
-            *reinterpret_cast<float4*>(si.ks) = make_float4(ks, ks, ks, ks);
-            *reinterpret_cast<float4*>(si.lv) = make_float4(lv, lv, lv, lv);
-            *reinterpret_cast<float4*>(si.iv) = make_float4(iv, iv, iv, iv);
-          } else {
-            for (int e = 0; e < 4 >> lppt; ++e) {
-              const int slot = in_tile * (4 >> lppt) + e;
-              si.ks[slot] = ks;
-              si.lv[slot] = lv;
-              si.iv[slot] = iv;
-            }
+          for (int e = 0; e < box / 16; ++e) {
+            const int slot = in_tile * (box / 16) + e;
+            si.ks[slot] = ks;
+            si.lv[slot] = lv;
+            si.iv[slot] = iv;
           }
           if (in_tile == 0) {
-            *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, head, row0, cur.tile * kTile);
+            *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, cur.head, cur.row0, cur.tile * kTile);
             *reinterpret_cast<int4*>(&si.len) = make_int4(lens[cur.seq], flags, cur.tiles, 0);
           }
         }
@@ -331,8 +338,8 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (wb == w0)   // the first tiles' copies do not wait for their scales
         for (; t < n_here && t < stages; ++t) issue(t, t);
       ks = cur.id >= 0 ? cur.ks : 0.f;
-      lv = log2f(cur.vs);
-      iv = 1.f / cur.vs;
+      lv = __log2f(cur.vs);      // (both exact for a power of two)
+      iv = __frcp_rn(cur.vs);
       for (int i = 0; i < t; ++i) publish(i, i);
       if (wb == w0) {
         issued = t;
@@ -361,17 +368,74 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  // ---------------- consumers: warp w takes tokens 16 w .. 16 w + 15 of each tile
-  const int g = lane >> 2, t4 = lane & 3;
-  const int krow = ((16 * warp) >> lbox) * 2 * box + ((16 * warp) & (box - 1));   // of the warp's tokens in a stage
-  // sequences without tokens: zero rows
-  for (int s = cta; s < a.B; s += gridDim.x)
-    if (first[s + 1] == first[s]) {
-      uint4* o = reinterpret_cast<uint4*>(static_cast<Tin*>(a.out) + (size_t)s * a.n_q * a.Hq * D);
-      const int n16 = a.n_q * a.Hq * D * (int)sizeof(Tin) / 16;
-      for (int i = tid; i < n16; i += 32 * kWarps) o[i] = make_uint4(0u, 0u, 0u, 0u);
+  const int n_tiles = (int)(w1 - w0);
+  if (warp == kWarps + 1) {   // ---------------- output
+    // sequences without tokens: zero rows
+    for (int s = cta; s < a.B; s += gridDim.x)
+      if (first[s + 1] == first[s]) {
+        uint4* o = reinterpret_cast<uint4*>(static_cast<Tin*>(a.out) + (size_t)s * a.n_q * a.Hq * D);
+        const int n16 = a.n_q * a.Hq * D * (int)sizeof(Tin) / 16;
+        for (int i = lane; i < n16; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
+      }
+    if (lane == 0) a.split[cta] = make_int4(-1, 0, 0, 0);   // (the same thread writes it again)
+    // joins the four warps' parts of each unit's stretch
+    for (int done = 0, use = 0; done < n_tiles; ++use) {
+      if (!warp_all(mbar_wait(parts_full, use & 1, wc, wsite(4, 0, done)))) return;
+      const UnitInfo u = *unit_info;
+      done = u.k + 1;
+      const int n_rows = min(kRows, a.rows - u.row0);
+      const bool begins = u.flags & kBegins, whole = begins && (u.flags & kEnds);
+      const int place = 2 * cta + (begins ? 1 : 0);   // of a part of a unit that goes on, or that an earlier CTA began
+#pragma unroll 2
+      for (int v = lane; v < n_rows * (D / 4); v += 32) {
+        const int r = v / (D / 4), c = v % (D / 4);
+        float2 ml[kWarps];
+        float m = kNoRef, l = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          ml[w] = *reinterpret_cast<const float2*>(red_ml + (w * part_rows + r) * 2);
+          m = fmaxf(m, ml[w].x);
+        }
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float f = ex2(ml[w].x - m);
+          const float4 x = *reinterpret_cast<const float4*>(red + (w * part_rows + r) * D + 4 * c);
+          l = fmaf(f, ml[w].y, l);
+          acc.x = fmaf(f, x.x, acc.x); acc.y = fmaf(f, x.y, acc.y);
+          acc.z = fmaf(f, x.z, acc.z); acc.w = fmaf(f, x.w, acc.w);
+        }
+        if (whole) {
+          const float il = l == 0.f ? 0.f : 1.f / l;   // (a row that sees nothing is zero)
+          const int row = u.row0 + r, i = row / a.G, h = u.head * a.G + row - i * a.G;
+          Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
+          if (sizeof(Tin) == 2)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * il, acc.y * il), pack_bf16(acc.z * il, acc.w * il));
+          else
+            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * il, acc.y * il, acc.z * il, acc.w * il);
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((size_t)place * kMaxRows + r) * D + 4 * c) = acc;
+          if (c == 0) {
+            a.part_ml[(size_t)place * 2 * kMaxRows + r] = m;
+            a.part_ml[(size_t)place * 2 * kMaxRows + kMaxRows + r] = l;
+          }
+        }
+      }
+      if (!(u.flags & kEnds) && lane == 0) {   // the unit goes on in later stretches
+        const long long w = w0 + u.k - u.tile;   // its first tile
+        a.split[cta] = make_int4(u.seq, u.head * a.row_tiles + u.row0 / kMaxRows, stretch_of(W, w, n_cta), stretch_of(W, w + u.tiles - 1, n_cta));
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(parts_empty);
     }
+    return;
+  }
 
+  // ---------------- consumers: a warp takes kSlices times 16 tokens of each tile
+  constexpr int kSlices = kTile / 16 / kWarps;
+  const int g = lane >> 2, t4 = lane & 3;
+  const int slot = kSlices * warp;      // the warp's first 16 tokens of a tile
+  const int krow = ((16 * slot) >> lbox) * 2 * box + ((16 * slot) & (box - 1)), kslice = box == 16 ? 32 : 16;   // their key rows in a stage, and from there to the next 16's
   constexpr int KS = D / 16;            // k-steps of the first product
   constexpr int MT = D / 16;            // 16-row tiles of O^T
   uint32_t qf[NT][KS][2], ql[kSplit ? NT : 1][kSplit ? KS : 1][2];   // Q^T operands (and the rows' low terms)
@@ -380,23 +444,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   int lim[NT][2];                       // tokens that a row sees
   int row0 = 0;
   bool begins = false;                  // the CTA's stretch of the unit starts with its first tile
-  uint32_t joins = 0;
-  // barrier `b` of all consumer warps (bounded, as every wait: a warp that gave up frees the others)
-  auto arrive = [&](int b) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&joined[b]);
-  };
-  auto wait_for = [&](int b, uint32_t use, int k) { return warp_all(mbar_wait(&joined[b], use & 1, wc, wsite(3, b, k))); };
-  const int n_tiles = (int)(w1 - w0);
+  uint32_t units_done = 0;
   for (int k = 0, st = 0, phase = 0; k < n_tiles; ++k) {
     if (!warp_all(mbar_wait(&full[st], phase, wc, wsite(2, st, k)))) return;
     const StageInfo& si = info[st];
     const char* sk = smem + st * S::STAGE;
-    const int flags = si.flags, len = si.len, tok = si.tok0 + 16 * warp;
+    const int flags = si.flags, len = si.len, tok = si.tok0 + 16 * slot;
     if (flags & kFirst) {
       row0 = si.row0;
       begins = (flags & kBegins) != 0;
-      const char* sq = sk + 2 * S::KV;
+      const char* sq = sk + S::KV;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         // row g of this eight: the thread's d are those whose key bytes it reads (16-byte column c = word j / 4)
@@ -451,155 +508,200 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
       }
     }
-    const float ks = si.ks[warp], lv = si.lv[warp], iv = si.iv[warp];
-    if (tok < len && ks != 0.f) {
-      // keys: rows g and g + 8 of the warp's 16 tokens
-      const int r0 = krow + token_of(g);
-      uint32_t kw[2][KS];
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int c = 0; c < KS / 4; ++c) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sk + swz<D>(r0 + 8 * r, (D == 128 ? 2 * t4 + c : t4) * 16));
-          kw[r][4 * c] = u.x; kw[r][4 * c + 1] = u.y; kw[r][4 * c + 2] = u.z; kw[r][4 * c + 3] = u.w;
-        }
-      float s[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) s[n][c] = 0.f;
-#pragma unroll
-      for (int j = 0; j < KS; ++j) {
-        uint32_t a0, a1, a2, a3;
-        codes_to_f16<T>(kw[0][j], a0, a2);
-        codes_to_f16<T>(kw[1][j], a1, a3);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          mma16816(s[n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
-          if (kSplit)
-            mma16816(s[n], a0, a1, a2, a3, ql[kSplit ? n : 0][kSplit ? j : 0][0], ql[kSplit ? n : 0][kSplit ? j : 0][1]);
-        }
-      }
-      // to log2 units, with the value scale; tokens that a row does not see
-      const bool edge = tok + 16 > len - a.n_q + 1;
-      bool raise = false;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          s[n][c] = fmaf(s[n][c], ks * rs[n][c & 1], lv);
-          if (edge && tok + 8 * (c >> 1) + token_of(g) >= lim[n][c & 1]) s[n][c] = -INFINITY;
-          raise |= s[n][c] > ref[n][c & 1] + kRaiseAt;
-        }
-      if (__any_sync(0xffffffffu, raise)) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float f[2];
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float top = fmaxf(s[n][c], s[n][c + 2]);
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-            const float to = fmaxf(ref[n][c], top - kRefBelow);
-            f[c] = ex2(ref[n][c] - to);
-            ref[n][c] = to;
-            sum[n][c] *= f[c];
-          }
-#pragma unroll
-          for (int i = 0; i < MT; ++i) {
-            o[n][i][0] *= f[0]; o[n][i][1] *= f[1];
-            o[n][i][2] *= f[0]; o[n][i][3] *= f[1];
-          }
-        }
-      }
-      float p[NT][4];
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) p[n][c] = ex2(s[n][c] - ref[n][c & 1]);
-        sum[n][0] = fmaf(p[n][0] + p[n][2], iv, sum[n][0]);
-        sum[n][1] = fmaf(p[n][1] + p[n][3], iv, sum[n][1]);
-      }
-      // values: this thread's four tokens, D / 8 bytes at column g
-      uint32_t vw[4][D / 32];
-#pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        const int row = krow + box + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
-        if (D == 128) {
-          const uint4 u = *reinterpret_cast<const uint4*>(sk + swz<D>(row, g * 16));
-          vw[r][0] = u.x; vw[r][1] = u.y; vw[r][D / 32 - 2] = u.z; vw[r][D / 32 - 1] = u.w;
-        } else {
-          const uint2 u = *reinterpret_cast<const uint2*>(sk + swz<D>(row, g * 8));
-          vw[r][0] = u.x; vw[r][1] = u.y;
-        }
-      }
-      // O^T += V^T P^T.  At the sequence's end (edge) there is one pass for each new token, over the value
-      // codes that it sees, and only its rows take the sums: with weights of zero alone, a NaN code behind
-      // a row's last visible token would reach it.
-      auto weigh = [&](auto at_end, int sees) {
+    {
+      // One or two slices of 16 tokens: `u` the first, its first token `at`.  At the sequence's end (at_end), or where a
+      // slice has no block, they are taken one by one and masked.
+      auto slices = [&](auto count, auto at_end, int u, int at) {
+        constexpr int NS = decltype(count)::value;
         constexpr bool kEdge = decltype(at_end)::value;
-        uint32_t pb[NT][2], pl[kSplit ? NT : 1][2];   // P^T operands (and their low terms)
+        float s[NS][NT][4];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          const uint32_t h0 = pack_f16(p[n][0], p[n][1]), h1 = pack_f16(p[n][2], p[n][3]);
-          pb[n][0] = transpose8x8(h0);
-          pb[n][1] = transpose8x8(h1);
-          if (kSplit) {
-            const float2 x = unpack_f16(h0), y = unpack_f16(h1);
-            pl[kSplit ? n : 0][0] = transpose8x8(pack_f16(p[n][0] - x.x, p[n][1] - x.y));
-            pl[kSplit ? n : 0][1] = transpose8x8(pack_f16(p[n][2] - y.x, p[n][3] - y.y));
-          }
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) s[i][n][c] = 0.f;
+        {
+          uint32_t kw[NS][2][KS];   // keys: rows g and g + 8 of the 16 tokens
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+#pragma unroll
+              for (int c = 0; c < KS / 4; ++c) {
+                const int row = krow + (u + i) * kslice + token_of(g) + 8 * r;
+                const uint4 x = *reinterpret_cast<const uint4*>(sk + swz<D>(row, (D == 128 ? 2 * t4 + c : t4) * 16));
+                kw[i][r][4 * c] = x.x; kw[i][r][4 * c + 1] = x.y; kw[i][r][4 * c + 2] = x.z; kw[i][r][4 * c + 3] = x.w;
+              }
+#pragma unroll
+          for (int j = 0; j < KS; ++j)
+#pragma unroll
+            for (int i = 0; i < NS; ++i) {
+              uint32_t a0, a1, a2, a3;
+              codes_to_f16<T>(kw[i][0][j], a0, a2);
+              codes_to_f16<T>(kw[i][1][j], a1, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                mma16816(s[i][n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+                if (kSplit)
+                  mma16816(s[i][n], a0, a1, a2, a3, ql[kSplit ? n : 0][kSplit ? j : 0][0], ql[kSplit ? n : 0][kSplit ? j : 0][1]);
+              }
+            }
         }
-        bool seen[4];   // of the thread's four tokens
-        if (kEdge)
+        // to log2 units with the value scale, from the row's reference; tokens that a row does not see
+        auto hidden = [&](int n, int c) { return kEdge && at + 8 * (c >> 1) + token_of(g) >= lim[n][c & 1]; };
+        float p[NS][NT][4];
+        float top = -INFINITY;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) seen[r] = tok + 8 * (r >> 1) + token_of(2 * t4 + (r & 1)) < sees;
+        for (int i = 0; i < NS; ++i) {
+          const float ks = si.ks[slot + u + i], lv = si.lv[slot + u + i];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          const uint32_t v0 = !kEdge || seen[0] ? vw[0][c] : 0u, v1 = !kEdge || seen[1] ? vw[1][c] : 0u;
-          const uint32_t v2 = !kEdge || seen[2] ? vw[2][c] : 0u, v3 = !kEdge || seen[3] ? vw[3][c] : 0u;
-          // bytes of the same d from the tokens of a pair, side by side
-          const uint32_t lo01 = __byte_perm(v0, v1, 0x5140), hi01 = __byte_perm(v0, v1, 0x7362);
-          const uint32_t lo23 = __byte_perm(v2, v3, 0x5140), hi23 = __byte_perm(v2, v3, 0x7362);
-          uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
-          codes_to_f16<T>(lo01, a0, a1);
-          codes_to_f16<T>(lo23, a2, a3);
-          codes_to_f16<T>(hi01, b0, b1);
-          codes_to_f16<T>(hi23, b2, b3);
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              p[i][n][c] = hidden(n, c) ? -INFINITY : fmaf(s[i][n][c], ks * rs[n][c & 1], lv - ref[n][c & 1]);
+              top = fmaxf(top, p[i][n][c]);
+            }
+        }
+        if (__any_sync(0xffffffffu, top > kRaiseAt)) {
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            float x[2][4];
+            float f[2];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) { x[0][e] = o[n][2 * c][e]; x[1][e] = o[n][2 * c + 1][e]; }
-            mma16816(x[0], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-            mma16816(x[1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
-            if (kSplit) {
-              mma16816(x[0], a0, a1, a2, a3, pl[kSplit ? n : 0][0], pl[kSplit ? n : 0][1]);
-              mma16816(x[1], b0, b1, b2, b3, pl[kSplit ? n : 0][0], pl[kSplit ? n : 0][1]);
+            for (int c = 0; c < 2; ++c) {
+              float m = -INFINITY;
+#pragma unroll
+              for (int i = 0; i < NS; ++i)
+#pragma unroll
+                for (int e = c; e < 4; e += 2) {
+                  p[i][n][e] = hidden(n, e) ? -INFINITY : fmaf(s[i][n][e], si.ks[slot + u + i] * rs[n][c], si.lv[slot + u + i]);
+                  m = fmaxf(m, p[i][n][e]);
+                }
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
+              m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
+              const float to = fmaxf(ref[n][c], m - kRefBelow);
+              f[c] = ex2(ref[n][c] - to);
+              ref[n][c] = to;
+              sum[n][c] *= f[c];
+#pragma unroll
+              for (int i = 0; i < NS; ++i)
+#pragma unroll
+                for (int e = c; e < 4; e += 2) p[i][n][e] -= to;
             }
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (!kEdge || lim[n][e & 1] == sees) { o[n][2 * c][e] = x[0][e]; o[n][2 * c + 1][e] = x[1][e]; }
+            for (int i = 0; i < MT; ++i) {
+              o[n][i][0] *= f[0]; o[n][i][1] *= f[1];
+              o[n][i][2] *= f[0]; o[n][i][3] *= f[1];
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          const float iv = si.iv[slot + u + i];
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[i][n][c] = ex2(p[i][n][c]);
+            sum[n][0] = fmaf(p[i][n][0] + p[i][n][2], iv, sum[n][0]);
+            sum[n][1] = fmaf(p[i][n][1] + p[i][n][3], iv, sum[n][1]);
+          }
+        }
+        // O^T += V^T P^T.  At the end there is one pass for each new token, over the value codes that it sees, and only its
+        // rows take the sums: with weights of zero alone, a NaN code behind a row's last visible token would reach it.
+#pragma unroll
+        for (int i = 0; i < NS; ++i) {
+          uint32_t pb[NT][2], pl[kSplit ? NT : 1][2];   // P^T operands (and their low terms)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float* x = p[i][n];
+            const uint32_t h0 = pack_f16(x[0], x[1]), h1 = pack_f16(x[2], x[3]);
+            pb[n][0] = transpose8x8(h0);
+            pb[n][1] = transpose8x8(h1);
+            if (kSplit) {
+              const float2 y0 = unpack_f16(h0), y1 = unpack_f16(h1);
+              pl[kSplit ? n : 0][0] = transpose8x8(pack_f16(x[0] - y0.x, x[1] - y0.y));
+              pl[kSplit ? n : 0][1] = transpose8x8(pack_f16(x[2] - y1.x, x[3] - y1.y));
+            }
+          }
+          // values: this thread's four tokens, D / 8 bytes at column g
+          uint32_t vw[4][D / 32];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = krow + (u + i) * kslice + box + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
+            if (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(sk + swz<D>(row, g * 16));
+              vw[r][0] = x.x; vw[r][1] = x.y; vw[r][D / 32 - 2] = x.z; vw[r][D / 32 - 1] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(sk + swz<D>(row, g * 8));
+              vw[r][0] = x.x; vw[r][1] = x.y;
+            }
+          }
+          auto weigh = [&](int sees) {
+            bool seen[4];   // of the thread's four tokens
+#pragma unroll
+            for (int r = 0; r < 4; ++r) seen[r] = !kEdge || at + 8 * (r >> 1) + token_of(2 * t4 + (r & 1)) < sees;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+              const uint32_t v0 = seen[0] ? vw[0][c] : 0u, v1 = seen[1] ? vw[1][c] : 0u;
+              const uint32_t v2 = seen[2] ? vw[2][c] : 0u, v3 = seen[3] ? vw[3][c] : 0u;
+              // bytes of the same d from the tokens of a pair, side by side
+              const uint32_t lo01 = __byte_perm(v0, v1, 0x5140), hi01 = __byte_perm(v0, v1, 0x7362);
+              const uint32_t lo23 = __byte_perm(v2, v3, 0x5140), hi23 = __byte_perm(v2, v3, 0x7362);
+              uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+              codes_to_f16<T>(lo01, a0, a1);
+              codes_to_f16<T>(lo23, a2, a3);
+              codes_to_f16<T>(hi01, b0, b1);
+              codes_to_f16<T>(hi23, b2, b3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n) {
+                float x[2][4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { x[0][e] = o[n][2 * c][e]; x[1][e] = o[n][2 * c + 1][e]; }
+                mma16816(x[0], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                mma16816(x[1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+                if (kSplit) {
+                  mma16816(x[0], a0, a1, a2, a3, pl[kSplit ? n : 0][0], pl[kSplit ? n : 0][1]);
+                  mma16816(x[1], b0, b1, b2, b3, pl[kSplit ? n : 0][0], pl[kSplit ? n : 0][1]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (!kEdge || lim[n][e & 1] == sees) { o[n][2 * c][e] = x[0][e]; o[n][2 * c + 1][e] = x[1][e]; }
+              }
+            }
+          };
+          if (!kEdge) {
+            weigh(0);
+          } else {
+#pragma unroll 1
+            for (int sees = max(len - a.n_q + 1, at + 1); sees <= len; ++sees) weigh(sees);
           }
         }
       };
-      if (!edge) {
-        weigh(std::false_type{}, 0);
+      using One = std::integral_constant<int, 1>;
+      // two slices side by side where there are two and their operands fit the registers
+      constexpr int kSide = kSlices > 1 && NT * D <= 128 ? 2 : 1;
+      bool whole = tok + 16 * kSlices <= len - a.n_q + 1;
+#pragma unroll
+      for (int u = 0; u < kSlices; ++u) whole = whole && si.ks[slot + u] != 0.f;
+      if (whole) {
+#pragma unroll 1
+        for (int u = 0; u < kSlices; u += kSide) slices(std::integral_constant<int, kSide>{}, std::false_type{}, u, 0);
       } else {
 #pragma unroll 1
-        for (int sees = max(len - a.n_q + 1, tok + 1); sees <= len; ++sees) weigh(std::true_type{}, sees);
+        for (int u = 0; u < kSlices; ++u)
+          if (tok + 16 * u < len && si.ks[slot + u] != 0.f) slices(One{}, std::true_type{}, u, tok + 16 * u);
       }
     }
-    const int seq = si.seq, head = si.head, tile = si.tok0 / kTile, tiles = si.tiles;
+    UnitInfo u{si.seq, si.head, row0, (flags & kEnds) | (begins ? kBegins : 0), si.tok0 / kTile, si.tiles, k, 0};
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
     if (++st == stages) { st = 0; phase ^= 1; }
 
-    if (flags & kLast) {
-      // join the four warps' parts of this stretch of the unit
-      const int n_rows = min(kRows, a.rows - row0);
-      if (joins > 0 && !wait_for(1, joins - 1, k)) return;   // the last unit's parts have been read
+    if (flags & kLast) {   // this stretch of the unit ends: the warp's part to the output's warp
+      if (units_done > 0 && !warp_all(mbar_wait(parts_empty, (units_done - 1) & 1, wc, wsite(3, 0, k)))) return;
+      ++units_done;
+      if (tid == 0) *unit_info = u;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -608,61 +710,18 @@ __global__ void __launch_bounds__(kThreads, 2)
           l += __shfl_xor_sync(0xffffffffu, l, 4);
           l += __shfl_xor_sync(0xffffffffu, l, 8);
           l += __shfl_xor_sync(0xffffffffu, l, 16);
-          if (g == 0) {
-            red_ml[(warp * kRows + 8 * n + 2 * t4 + c) * 2] = ref[n][c];
-            red_ml[(warp * kRows + 8 * n + 2 * t4 + c) * 2 + 1] = l;
-          }
-          // O^T: the thread holds d = 2 MT g .. 2 MT g + 2 MT - 1 of the row
-          if (8 * n + 2 * t4 + c < n_rows) {
-            float* dst = red + (size_t)(warp * kRows + 8 * n + 2 * t4 + c) * D + 2 * MT * g;
+          const int r = 8 * n + 2 * t4 + c;
+          if (r < part_rows) {   // (rows behind the unit's last one are written and not read)
+            if (g == 0) *reinterpret_cast<float2*>(red_ml + (warp * part_rows + r) * 2) = make_float2(ref[n][c], l);
+            // O^T: the thread holds d = 2 MT g .. 2 MT g + 2 MT - 1 of the row
+            float* dst = red + (warp * part_rows + r) * D + 2 * MT * g;
 #pragma unroll
             for (int i = 0; i < MT; i += 2)
-              *reinterpret_cast<float4*>(dst + 2 * i) =
-                  make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
+              *reinterpret_cast<float4*>(dst + 2 * i) = make_float4(o[n][i][c], o[n][i][c + 2], o[n][i + 1][c], o[n][i + 1][c + 2]);
           }
         }
-      arrive(0);
-      if (!wait_for(0, joins, k)) return;
-      const bool whole = begins && (flags & kEnds);
-      const bool carries_on = !begins;              // part of a unit that an earlier CTA began
-      const int slot = 2 * cta + (carries_on ? 0 : 1);
-      for (int v = tid; v < n_rows * (D / 4); v += 32 * kWarps) {
-        const int r = v / (D / 4), c = v % (D / 4);
-        float m = kNoRef;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_ml[(w * kRows + r) * 2]);
-        float l = 0.f;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2(red_ml[(w * kRows + r) * 2] - m);
-          l = fmaf(f, red_ml[(w * kRows + r) * 2 + 1], l);
-          const float4 x = *reinterpret_cast<const float4*>(red + (size_t)(w * kRows + r) * D + 4 * c);
-          acc.x = fmaf(f, x.x, acc.x); acc.y = fmaf(f, x.y, acc.y);
-          acc.z = fmaf(f, x.z, acc.z); acc.w = fmaf(f, x.w, acc.w);
-        }
-        if (whole) {
-          const float il = l == 0.f ? 0.f : 1.f / l;   // (a row that sees nothing is zero)
-          const int row = row0 + r, i = row / a.G, h = head * a.G + row - i * a.G;
-          Tin* dst = static_cast<Tin*>(a.out) + (((size_t)seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
-          if (sizeof(Tin) == 2)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * il, acc.y * il), pack_bf16(acc.z * il, acc.w * il));
-          else
-            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * il, acc.y * il, acc.z * il, acc.w * il);
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + ((size_t)slot * kMaxRows + r) * D + 4 * c) = acc;
-          if (c == 0) {
-            a.part_ml[(size_t)slot * 2 * kMaxRows + r] = m;
-            a.part_ml[(size_t)slot * 2 * kMaxRows + kMaxRows + r] = l;
-          }
-        }
-      }
-      if (!(flags & kEnds) && tid == 0) {   // the unit goes on in later stretches
-        const long long w = w0 + k - tile;  // its first tile
-        a.split[cta] = make_int4(seq, head * a.row_tiles + row0 / kMaxRows, stretch_of(W, w, n_cta), stretch_of(W, w + tiles - 1, n_cta));
-      }
-      arrive(1);
-      ++joins;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(parts_full);
     }
   }
 }

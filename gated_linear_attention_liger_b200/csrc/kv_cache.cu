@@ -170,14 +170,14 @@ liger_status launch_attn(const CUtensorMap& tm, const liger::ca::Args& a, int ct
   using S = liger::ca::Smem<Tin, D, NT>;
   // shared memory of one CTA with two on an SM (228 KB, 1 KB of it the system's, each), else alone
   constexpr int kShare = (228 * 1024) / kCtasPerSm - 1024, kAlone = 227 * 1024;
-  const int fixed = (int)S::bytes(0, a.B);
+  const int fixed = (int)S::bytes(0, a.rows, a.B);
   int stages = (kShare - fixed) / (int)S::STAGE;
   if (stages < 3) {   // thousands of sequences: their prefix sums take the second CTA's place
     stages = (kAlone - fixed) / (int)S::STAGE;
     ctas /= kCtasPerSm;
   }
   if (stages > S::MAX_STAGES) stages = S::MAX_STAGES;
-  const int smem = (int)S::bytes(stages, a.B);
+  const int smem = (int)S::bytes(stages, a.rows, a.B);
   auto kern = liger::ca::cached_attn_kernel<Tin, D, T, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cached attention)");
@@ -285,7 +285,8 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   const int per16 = dt == LIGER_BF16 ? 8 : 4;
   if (q_stride < (long long)Hq * d || q_stride % per16)
     return fail(LIGER_ERR_INVALID_ARG, "the query's token stride must be at least Hq * d elements and a multiple of 16 bytes");
-  const long long tiles = (long long)B * (((long long)table_width * block_size + liger::ca::kTile - 1) / liger::ca::kTile);
+  const int tile = liger::ca::tile_tokens(d);
+  const long long tiles = (long long)B * (((long long)table_width * block_size + tile - 1) / tile);
   if ((long long)n_blocks * Hkv > 0x7fffffffLL || tiles > 0x7fffffffLL)
     return fail(LIGER_ERR_UNSUPPORTED, "cache too large");
   if (!q || !cache || !scales || !block_table || !seq_lens || !out)
@@ -305,7 +306,7 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   const auto enc = liger::tensor_map_encoder();
   const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)block_size, 2, (cuuint64_t)n_blocks * Hkv};
   const cuuint64_t strides[3] = {(cuuint64_t)d, (cuuint64_t)block_size * d, (cuuint64_t)2 * block_size * d};
-  const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)(block_size < liger::ca::kTile ? block_size : liger::ca::kTile), 2, 1};
+  const cuuint32_t box[4] = {(cuuint32_t)d, (cuuint32_t)(block_size < tile ? block_size : tile), 2, 1};
   const cuuint32_t es[4] = {1, 1, 1, 1};
   if (!enc || enc(&tm, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(cache), dims, strides, box, es,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
