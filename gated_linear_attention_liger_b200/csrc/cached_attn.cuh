@@ -92,7 +92,7 @@ constexpr int tile_tokens(int d) { return 8192 / d; }
 // What the consumer warps tell the output's warp about the unit that they have just ended.
 struct UnitInfo {
   int seq, head, row0, flags;
-  int tile, tiles, k, pad;             // the last tile's number in the unit, the unit's tiles, the tile's number in the stretch
+  int tiles, k, pad0, pad1;            // the unit's tiles; the last one's number in the stretch
 };
 
 // Shared memory.  NT: query rows in eights (1 or 2).
@@ -102,11 +102,11 @@ struct Smem {
   static constexpr uint32_t Q = 8 * NT * D * sizeof(Tin);
   static constexpr uint32_t STAGE = KV + Q;                       // a multiple of 1024
   static constexpr int MAX_STAGES = 12;
-  static constexpr uint32_t FIXED = MAX_STAGES * (sizeof(StageInfo) + 16) + sizeof(UnitInfo) + 16 + 64;
+  static constexpr uint32_t FIXED = MAX_STAGES * (sizeof(StageInfo) + 16) + sizeof(UnitInfo) + 16 + 80;
   static __host__ __device__ int part_rows(int rows) { return rows < 8 * NT ? rows : 8 * NT; }
-  // the four warps' parts of a unit: sums, then references and sums of weights
-  static __host__ __device__ uint32_t red(int rows) { return kWarps * part_rows(rows) * (D * 4 + 8); }
-  static uint32_t bytes(int stages, int rows, int B) { return 1024 + stages * STAGE + FIXED + (red(rows) + 15) / 16 * 16 + 4 * (2 * B + 1); }
+  // the four warps' parts of a unit: sums, then references and sums of weights; then the parts' weights
+  static __host__ __device__ uint32_t red(int rows) { return kWarps * part_rows(rows) * (D * 4 + 8 + 4); }
+  static uint32_t bytes(int stages, int rows, int B) { return 1024 + stages * STAGE + FIXED + (red(rows) + 15) / 16 * 16 + 4 * (3 * B + 2); }
 };
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
@@ -166,10 +166,17 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// First tile of CTA c's stretch of the line of W tiles.
-__device__ __forceinline__ long long stretch_begin(long long W, int c, int n) { return W * c / n; }
-// The CTA whose stretch holds tile w.
-__device__ __forceinline__ int stretch_of(long long W, long long w, int n) { return (int)(((w + 1) * n - 1) / W); }
+// The line of work: sequence by sequence, unit by unit, a place for each tile and kUnitCost more behind a unit's last one
+// (its query operands and its output cost that much), cut into n equal stretches.  n is at most the line's length, so
+// that the tiles of one unit lie in consecutive stretches.
+constexpr int kUnitCost = 2;
+// a / b of numbers that are not negative, in 32 bits where they fit (the long division takes several times as long)
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
+}
+__device__ __forceinline__ long long cut(long long W, int c, int n) { return quotient(W * c, n); }
+// The stretch that holds place w.
+__device__ __forceinline__ int stretch_of(long long W, long long w, int n) { return (int)quotient((w + 1) * n - 1, W); }
 
 template <typename Tin, int D, KvType T, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -185,14 +192,16 @@ __global__ void __launch_bounds__(kThreads, 2)
   uint64_t* empty = full + S::MAX_STAGES;
   uint64_t* parts_full = empty + S::MAX_STAGES;                       // the warps' parts are written
   uint64_t* parts_empty = parts_full + 1;                             // and read
-  int* part = reinterpret_cast<int*>(parts_empty + 1);                // [6] warp sums of the scan
-  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(part + 8);
+  int* part = reinterpret_cast<int*>(parts_empty + 1);                // [2][8] warp sums of the scan
+  volatile uint32_t* abort_flag = reinterpret_cast<uint32_t*>(part + 16);
   volatile uint32_t* never = abort_flag + 1;
   const int part_rows = S::part_rows(a.rows);
-  float* red = reinterpret_cast<float*>(part + 16);                   // [kWarps][part_rows][D]
+  float* red = reinterpret_cast<float*>(part + 20);                   // [kWarps][part_rows][D]
   float* red_ml = red + kWarps * part_rows * D;                       // [kWarps][part_rows][2]
-  int* first = reinterpret_cast<int*>(part + 16) + (S::red(a.rows) + 15) / 16 * 4;   // [B + 1] tiles before each sequence
-  int* lens = first + a.B + 1;                                        // [B]
+  float* wgt = red_ml + kWarps * part_rows * 2;                       // [part_rows][kWarps]
+  int* first = reinterpret_cast<int*>(part + 20) + (S::red(a.rows) + 15) / 16 * 4;   // [B + 1] tiles before each sequence
+  int* before = first + a.B + 1;                                      // [B + 1] sequences with tokens before each one
+  int* lens = before + a.B + 1;                                       // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -212,32 +221,52 @@ __global__ void __launch_bounds__(kThreads, 2)
   {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int s0 = tid * per, s1 = min(a.B, s0 + per);
-    int sum = 0;
+    int sum = 0, some = 0;
     for (int s = s0; s < s1; ++s) {
       const int len = min(max(a.lens[s], 0), cap), n = (int)(((long long)len + kTile - 1) / kTile);
       lens[s] = len;
-      first[s + 1] = n;
       sum += n;
+      some += n > 0;
     }
-    int x = sum;
+    int x = sum, y = some;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += u;
+      const int u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+      if (lane >= o) { x += u; y += v; }
     }
-    if (lane == 31) part[warp] = x;
+    if (lane == 31) { part[warp] = x; part[8 + warp] = y; }
     __syncthreads();
-    int run = x - sum;
-    for (int w = 0; w < warp; ++w) run += part[w];
-    if (tid == 0) first[0] = 0;
-    for (int s = s0; s < s1; ++s) { run += first[s + 1]; first[s + 1] = run; }
+    int run = x - sum, seqs = y - some;
+    for (int w = 0; w < warp; ++w) { run += part[w]; seqs += part[8 + w]; }
+    for (int s = s0; s < s1; ++s) {
+      const int n = (int)(((long long)lens[s] + kTile - 1) / kTile);
+      first[s] = run;
+      before[s] = seqs;
+      run += n;
+      seqs += n > 0;
+    }
+    if (s1 == a.B && s0 < a.B) { first[a.B] = run; before[a.B] = seqs; }
     __syncthreads();
   }
   const int units = a.Hkv * a.row_tiles;                     // of one sequence
-  const long long W = (long long)first[a.B] * units;
-  // as many CTAs as there are tiles, so that no stretch is empty (a unit's parts are those of consecutive CTAs)
+  auto places = [&](int s) { return ((long long)first[s] + (long long)kUnitCost * before[s]) * units; };   // before sequence s
+  const long long W = places(a.B);
   const int cta = blockIdx.x, n_cta = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
-  const long long w0 = cta < n_cta ? stretch_begin(W, cta, n_cta) : W, w1 = cta < n_cta ? stretch_begin(W, cta + 1, n_cta) : W;
+  // tiles before place w of the line
+  auto tiles_before = [&](long long w) {
+    int lo = 0, hi = a.B;   // places(lo) <= w, and w < places(hi) but at the end
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (places(mid) <= w) lo = mid;
+      else hi = mid;
+    }
+    const int n = first[lo + 1] - first[lo];
+    if (n == 0) return (long long)first[lo] * units;
+    const long long r = w - places(lo), unit = quotient(r, n + kUnitCost), in = r - unit * (n + kUnitCost);
+    return (long long)first[lo] * units + (unit < units ? unit * n + (in < n ? in : n) : (long long)units * n);
+  };
+  // the tiles of this CTA's stretch
+  const long long w0 = cta < n_cta ? tiles_before(cut(W, cta, n_cta)) : 0, w1 = cta < n_cta ? tiles_before(cut(W, cta + 1, n_cta)) : 0;
   const WaitCtx wc{abort_flag, a.err, a.wait_ns};
 
   const int bs = 1 << a.lbs, kLog = D == 128 ? 6 : 7, lbox = a.lbs < kLog ? a.lbs : kLog, box = 1 << lbox;   // rows of keys, and of values, of one copy
@@ -264,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         const long long r = w - (long long)first[lo] * units;
         it.seq = lo;
         it.tiles = first[lo + 1] - first[lo];
-        const int unit = r >> 32 ? (int)(r / it.tiles) : (int)((uint32_t)r / (uint32_t)it.tiles);
+        const int unit = (int)quotient(r, it.tiles);
         it.tile = (int)(r - (long long)unit * it.tiles);
         it.head = unit;
         if (a.row_tiles > 1) {
@@ -386,44 +415,52 @@ __global__ void __launch_bounds__(kThreads, 2)
       const int n_rows = min(kRows, a.rows - u.row0);
       const bool begins = u.flags & kBegins, whole = begins && (u.flags & kEnds);
       const int place = 2 * cta + (begins ? 1 : 0);   // of a part of a unit that goes on, or that an earlier CTA began
-#pragma unroll 2
-      for (int v = lane; v < n_rows * (D / 4); v += 32) {
-        const int r = v / (D / 4), c = v % (D / 4);
-        float2 ml[kWarps];
-        float m = kNoRef, l = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          ml[w] = *reinterpret_cast<const float2*>(red_ml + (w * part_rows + r) * 2);
-          m = fmaxf(m, ml[w].x);
-        }
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float f = ex2(ml[w].x - m);
-          const float4 x = *reinterpret_cast<const float4*>(red + (w * part_rows + r) * D + 4 * c);
-          l = fmaf(f, ml[w].y, l);
-          acc.x = fmaf(f, x.x, acc.x); acc.y = fmaf(f, x.y, acc.y);
-          acc.z = fmaf(f, x.z, acc.z); acc.w = fmaf(f, x.w, acc.w);
-        }
-        if (whole) {
-          const float il = l == 0.f ? 0.f : 1.f / l;   // (a row that sees nothing is zero)
-          const int row = u.row0 + r, i = row / a.G, h = u.head * a.G + row - i * a.G;
-          Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
-          if (sizeof(Tin) == 2)
-            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(acc.x * il, acc.y * il), pack_bf16(acc.z * il, acc.w * il));
-          else
-            *reinterpret_cast<float4*>(dst) = make_float4(acc.x * il, acc.y * il, acc.z * il, acc.w * il);
-        } else {
-          *reinterpret_cast<float4*>(a.part_o + ((size_t)place * kMaxRows + r) * D + 4 * c) = acc;
-          if (c == 0) {
+      // the parts' weights, a lane for each warp's part of a row
+      for (int at = 0; at < 4 * n_rows; at += 32) {
+        const int r = min((at + lane) >> 2, n_rows - 1), w = lane & 3;
+        const float2 ml = *reinterpret_cast<const float2*>(red_ml + (w * part_rows + r) * 2);
+        float m = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        const float f = ex2(ml.x - m);
+        float l = f * ml.y;
+        l += __shfl_xor_sync(0xffffffffu, l, 1);
+        l += __shfl_xor_sync(0xffffffffu, l, 2);
+        if (at + lane < 4 * n_rows) {
+          wgt[4 * r + w] = !whole ? f : (l == 0.f ? 0.f : f / l);   // (a row that sees nothing is zero)
+          if (!whole && w == 0) {
             a.part_ml[(size_t)place * 2 * kMaxRows + r] = m;
             a.part_ml[(size_t)place * 2 * kMaxRows + kMaxRows + r] = l;
           }
         }
       }
+      __syncwarp();
+#pragma unroll 4
+      for (int v = lane; v < n_rows * (D / 4); v += 32) {
+        const int r = v / (D / 4), c = v % (D / 4);
+        const float4 f = *reinterpret_cast<const float4*>(wgt + 4 * r);
+        const float* x = red + r * D + 4 * c;
+        const float4 x0 = *reinterpret_cast<const float4*>(x), x1 = *reinterpret_cast<const float4*>(x + part_rows * D);
+        const float4 x2 = *reinterpret_cast<const float4*>(x + 2 * part_rows * D), x3 = *reinterpret_cast<const float4*>(x + 3 * part_rows * D);
+        float4 y;
+        y.x = f.x * x0.x + f.y * x1.x + f.z * x2.x + f.w * x3.x;
+        y.y = f.x * x0.y + f.y * x1.y + f.z * x2.y + f.w * x3.y;
+        y.z = f.x * x0.z + f.y * x1.z + f.z * x2.z + f.w * x3.z;
+        y.w = f.x * x0.w + f.y * x1.w + f.z * x2.w + f.w * x3.w;
+        if (whole) {
+          const int row = u.row0 + r, i = row / a.G, h = u.head * a.G + row - i * a.G;
+          Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
+          if (sizeof(Tin) == 2)
+            *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
+          else
+            *reinterpret_cast<float4*>(dst) = y;
+        } else {
+          *reinterpret_cast<float4*>(a.part_o + ((size_t)place * kMaxRows + r) * D + 4 * c) = y;
+        }
+      }
       if (!(u.flags & kEnds) && lane == 0) {   // the unit goes on in later stretches
-        const long long w = w0 + u.k - u.tile;   // its first tile
-        a.split[cta] = make_int4(u.seq, u.head * a.row_tiles + u.row0 / kMaxRows, stretch_of(W, w, n_cta), stretch_of(W, w + u.tiles - 1, n_cta));
+        const int unit = u.head * a.row_tiles + u.row0 / kMaxRows;
+        const long long w = places(u.seq) + (long long)unit * (u.tiles + kUnitCost);   // its first tile's place
+        a.split[cta] = make_int4(u.seq, unit, stretch_of(W, w, n_cta), stretch_of(W, w + u.tiles - 1, n_cta));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(parts_empty);
@@ -693,7 +730,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (tok + 16 * u < len && si.ks[slot + u] != 0.f) slices(One{}, std::true_type{}, u, tok + 16 * u);
       }
     }
-    UnitInfo u{si.seq, si.head, row0, (flags & kEnds) | (begins ? kBegins : 0), si.tok0 / kTile, si.tiles, k, 0};
+    const UnitInfo u{si.seq, si.head, row0, (flags & kEnds) | (begins ? kBegins : 0), si.tiles, k, 0, 0};
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
     if (++st == stages) { st = 0; phase ^= 1; }

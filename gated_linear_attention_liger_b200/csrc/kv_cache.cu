@@ -123,11 +123,13 @@ cudaError_t launch_assign(const liger::kvc::AssignArgs& a, int ctas, cudaStream_
 
 template <typename Tin, KvType T, int D, int BS>
 cudaError_t launch_append(const liger::kvc::AppendArgs& a, cudaStream_t s) {
-  // One token a CTA while that is a few CTAs an SM; else 32, so that a prompt's tokens that lead
-  // no run do not cost a CTA each.
-  const int range = (long long)a.N * a.Hkv <= 32LL * liger::device_sm_count() ? 1 : 32;
-  const dim3 grid((unsigned)((a.N + range - 1) / range), (unsigned)a.Hkv);
-  return launch(liger::kvc::append_kernel<Tin, T, D, BS>, grid, liger::kvc::kAppendThreads, 0, s, a, range);
+  using S = liger::kvc::AppendShape<Tin, D, BS>;
+  // One token a CTA while that is a few CTAs an SM (each run then has its own); else a block's worth, so that a prompt's
+  // tokens that lead no run do not cost a CTA each.
+  const int heads = (a.Hkv + S::kHeads - 1) / S::kHeads;
+  const int range = (long long)a.N * heads <= 32LL * liger::device_sm_count() ? 1 : S::kRange;
+  const dim3 grid((unsigned)((a.N + range - 1) / range), (unsigned)heads);
+  return launch(liger::kvc::append_kernel<Tin, T, D, BS>, grid, S::kThreads, 0, s, a, range);
 }
 template <typename Tin, KvType T, int D>
 cudaError_t append_bs(const liger::kvc::AppendArgs& a, int bs, cudaStream_t s) {

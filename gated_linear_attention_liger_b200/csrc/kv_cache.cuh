@@ -11,6 +11,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 
 namespace liger {
@@ -261,7 +263,8 @@ struct AppendArgs {
   int N, Hkv, n_slots;      // n_slots = n_blocks * bs
 };
 
-// Eight elements of a row in fp32.
+// Eight elements of a row.  add_max gathers the largest magnitude's bits (magnitudes order like their bits), max_bits
+// gives them as fp32's.
 template <typename Tin> struct Eight;
 template <> struct Eight<__nv_bfloat16> {
   uint4 u;
@@ -275,42 +278,70 @@ template <> struct Eight<__nv_bfloat16> {
       x[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
     }
   }
+  __device__ __forceinline__ void add_max(uint32_t& m) const {   // two 16-bit maxima
+    m = __vmaxu2(m, u.x & 0x7FFF7FFFu);
+    m = __vmaxu2(m, u.y & 0x7FFF7FFFu);
+    m = __vmaxu2(m, u.z & 0x7FFF7FFFu);
+    m = __vmaxu2(m, u.w & 0x7FFF7FFFu);
+  }
+  static __device__ __forceinline__ uint32_t max_bits(uint32_t m) { return max(m & 0xFFFF0000u, m << 16); }
 };
 template <> struct Eight<float> {
-  float4 a, b;
+  uint4 a, b;
   __device__ __forceinline__ void load(const float* p) {
-    a = __ldg(reinterpret_cast<const float4*>(p));
-    b = __ldg(reinterpret_cast<const float4*>(p) + 1);
+    a = __ldg(reinterpret_cast<const uint4*>(p));
+    b = __ldg(reinterpret_cast<const uint4*>(p) + 1);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void zero() { a = b = make_uint4(0u, 0u, 0u, 0u); }
   __device__ __forceinline__ void get(float* x) const {
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w;
-    x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __uint_as_float(w[i]);
   }
+  __device__ __forceinline__ void add_max(uint32_t& m) const {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, w[i] & 0x7FFFFFFFu);
+  }
+  static __device__ __forceinline__ uint32_t max_bits(uint32_t m) { return m; }
 };
+constexpr uint32_t kInfBits = 0x7F800000u;
 
-// Largest finite magnitude, as bits (magnitudes order like their bits; infinities and NaN are left out).
-__device__ __forceinline__ uint32_t amax8(const float* x) {
+// Largest finite magnitude, as bits.
+__device__ __forceinline__ uint32_t finite_max8(const float* x) {
   uint32_t m = 0u;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const uint32_t b = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-    m = max(m, b < 0x7F800000u ? b : 0u);
+    m = max(m, b < kInfBits ? b : 0u);
   }
   return m;
 }
 
+// Codes of eight elements.  `plain`: the scale is a power of two (`inv` its reciprocal) and, for int8, all elements are
+// finite, so that |x / scale| <= 127 and adding 1.5 * 2^23 leaves the code, rounded to even, in the low byte.
 template <KvType T>
-__device__ __forceinline__ uint2 quantise8(const float* x, float scale, float inv, bool pow2) {
-  uint32_t c[4];
+__device__ __forceinline__ uint2 quantise8(const float* x, float scale, float inv, bool plain) {
+  uint32_t c[2];
+  if (plain && T == kInt8) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    // a scale that is no power of two (a cache from elsewhere) takes the exact division
-    const float lo = pow2 ? x[2 * i] * inv : __fdiv_rn(x[2 * i], scale);
-    const float hi = pow2 ? x[2 * i + 1] * inv : __fdiv_rn(x[2 * i + 1], scale);
-    c[i] = code2<T>(lo, hi);
+    for (int i = 0; i < 2; ++i) {
+      uint32_t y[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = __float_as_uint(fmaf(x[4 * i + e], inv, 12582912.f));
+      c[i] = __byte_perm(__byte_perm(y[0], y[1], 0x0040), __byte_perm(y[2], y[3], 0x0040), 0x5410);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      float y[4];
+      // a scale that is no power of two (a cache from elsewhere) takes the exact division
+#pragma unroll
+      for (int e = 0; e < 4; ++e) y[e] = plain ? x[4 * i + e] * inv : __fdiv_rn(x[4 * i + e], scale);
+      c[i] = code2<T>(y[0], y[1]) | (code2<T>(y[2], y[3]) << 16);
+    }
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return make_uint2(c[0], c[1]);
 }
 
 // Rows [0, rows) of one block half held under `old` again under `after` (after > old).
@@ -330,33 +361,43 @@ __device__ __forceinline__ void requantise(uint8_t* half, int rows, float old, f
   }
 }
 
-constexpr int kAppendThreads = 256;
-constexpr int kShortRun = 4;   // runs up to this many tokens are taken by one warp each
-
 // A run is a stretch of consecutive tokens with consecutive slots in one block: with the tokens of a
 // sequence in order, all the tokens that a call brings to that block.  Its first token leads
-// it.  CTA (x, h) finds the runs that start in its `range` tokens, for kv head h: a long run is taken by the
-// whole CTA (half of it the keys, half the values, every element held in registers between the maximum
-// and the codes, so that it is read once), short runs by one warp for each of keys and values.
+// it.  CTA (x, y) finds the runs that start in its `range` tokens and takes them for a few kv heads: the keys, or
+// the values, of a run and head go to a team of as many warps as hold a whole block's rows in registers between the
+// maximum and the codes (128 bytes a lane), so that they are read once; where a team has several warps, runs of a
+// few tokens go to single warps.
 // A run that starts at offset 0 gives the block its scale; another one raises the scale if it has to, and
 // the rows before it are then requantised under the new one.
 // What bounds it: HBM for prompts (one read, one write); latency for single tokens.
+template <typename Tin, int D, int BS>
+struct AppendShape {
+  static constexpr int kRowLanes = D / 8;                                       // lanes of a row, eight elements each
+  static constexpr int kTeam = BS * D * (int)sizeof(Tin) <= 4096 ? 1 : BS * D * (int)sizeof(Tin) / 4096;   // warps
+  static constexpr int kThreads = 2 * kTeam * 32 < 256 ? 256 : 2 * kTeam * 32;
+  static constexpr int kHeads = kThreads / (2 * kTeam * 32);                    // of a CTA
+  static constexpr int kPieces = BS * kRowLanes / (32 * kTeam);                 // eight elements each, of a thread
+  static constexpr int kRange = BS < 64 ? (BS < 32 ? 16 : 32) : 64;             // tokens of a CTA, when there are many
+};
+constexpr int kShortRun = 4;
+
 template <typename Tin, KvType T, int D, int BS>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, int range) {
-  constexpr int kVecRow = D / 8;                          // 8-element pieces of a row
-  constexpr int kHalf = kAppendThreads / 2;
-  constexpr int kPieces = (BS * kVecRow + kHalf - 1) / kHalf;   // of a thread, in a long run
-  constexpr int kWords = kAppendThreads / 32;
+__global__ void __launch_bounds__(AppendShape<Tin, D, BS>::kThreads, 1024 / AppendShape<Tin, D, BS>::kThreads)
+    append_kernel(AppendArgs a, int range) {
+  using S = AppendShape<Tin, D, BS>;
+  constexpr int kWindow = 256, kWords = kWindow / 32, kWarps = S::kThreads / 32;
+  static_assert(S::kRange + BS <= kWindow, "a run that starts in the CTA's tokens ends in its window");
   __shared__ uint32_t s_cont[kWords], s_valid[kWords];    // bit i: token r0 + i continues a run / has a slot
-  __shared__ uint32_t s_max[kWords];
-  const int h = blockIdx.y, tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  __shared__ int s_slot[kWindow];
+  __shared__ uint32_t s_max[2][kWarps];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int r0 = blockIdx.x * range;
   pdl_launch_next();
   pdl_wait_previous();
-  {
+  if (tid < kWindow) {
     const int i = r0 + tid;
     int slot = -1, prev = -1;
-    if (i < a.N && tid < range + BS) {
+    if (tid < range + BS && i < a.N) {
       slot = a.slots[i];
       prev = i > 0 ? a.slots[i - 1] : -1;
     }
@@ -364,6 +405,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
     const bool cont = valid && prev >= 0 && slot == prev + 1 && slot % BS != 0;
     const uint32_t bv = __ballot_sync(0xffffffffu, valid), bc = __ballot_sync(0xffffffffu, cont);
     if (lane == 0) { s_valid[warp] = bv; s_cont[warp] = bc; }
+    s_slot[tid] = slot;
   }
   __syncthreads();
   // tokens of the run that token i leads (at most BS: a run ends with its block)
@@ -378,7 +420,61 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
     }
     return n < BS ? n : BS;
   };
-  int n_short = 0;
+  // The keys (half 0) or values of tokens i .. i + n - 1 and head h, by `kTeamWarps` warps of which the calling thread is
+  // number t: kLoads pieces a thread.  `top` reduces a warp's maximum over the team.
+  auto take = [&](auto loads, auto team_warps, int i, int n, int h, int half, int t, auto top) {
+    constexpr int kLoads = decltype(loads)::value, kTeamWarps = decltype(team_warps)::value;
+    const int slot = s_slot[i], off = slot % BS;
+    const size_t unit = ((size_t)(slot / BS) * a.Hkv + h) * 2 + half;
+    const long stride = half ? a.vstride : a.kstride;
+    const Tin* src = static_cast<const Tin*>(half ? a.v : a.k) + (size_t)(r0 + i) * stride + (size_t)h * D + (t % S::kRowLanes) * 8;
+    const int row0 = t / S::kRowLanes;
+    constexpr int kStep = 32 * kTeamWarps / S::kRowLanes;   // rows from a thread's piece to its next
+    Eight<Tin> e[kLoads];
+    const float old = off ? a.scales[unit] : 0.f;
+#pragma unroll
+    for (int p = 0; p < kLoads; ++p) {
+      e[p].zero();
+      if (row0 + p * kStep < n) e[p].load(src + (size_t)(row0 + p * kStep) * stride);
+    }
+    uint32_t m = 0u;
+#pragma unroll
+    for (int p = 0; p < kLoads; ++p) e[p].add_max(m);
+    m = top(__reduce_max_sync(0xffffffffu, Eight<Tin>::max_bits(m)));   // (and every thread has read the old scale)
+    const bool finite = m < kInfBits;
+    if (!finite) {
+      m = 0u;
+#pragma unroll
+      for (int p = 0; p < kLoads; ++p) {
+        float x[8];
+        e[p].get(x);
+        m = max(m, finite_max8(x));
+      }
+      m = top(__reduce_max_sync(0xffffffffu, m));
+    }
+    float after = scale_for<T>(__uint_as_float(m));
+    if (off) after = fmaxf(after, old);
+    uint8_t* dst = a.cache + unit * (size_t)(BS * D);
+    if (off && after > old) requantise<T, D>(dst, off, old, after, t, 32 * kTeamWarps);
+    if (t == 0 && (!off || after > old)) a.scales[unit] = after;
+    const bool pow2 = (__float_as_uint(after) & 0x7FFFFFu) == 0u, plain = pow2 && (T == kE4m3 || finite);
+    const float inv = 1.f / after;
+    dst += (size_t)(off + row0) * D + (t % S::kRowLanes) * 8;
+    auto write = [&](bool as_plain) {
+#pragma unroll
+      for (int p = 0; p < kLoads; ++p) {
+        float x[8];
+        e[p].get(x);
+        if (row0 + p * kStep < n) *reinterpret_cast<uint2*>(dst + p * kStep * D) = quantise8<T>(x, after, inv, as_plain);
+      }
+    };
+    if (plain) write(true);
+    else write(false);
+  };
+  using std::integral_constant;
+  auto in_warp = [](uint32_t m) { return m; };
+  const int team = warp / S::kTeam, half = team & 1, h = blockIdx.y * S::kHeads + (team >> 1), t = tid - team * S::kTeam * 32;
+  int n_short = 0, n_long = 0;
   for (int w = 0; w * 32 < range; ++w) {
     uint32_t lead = s_valid[w] & ~s_cont[w];
     if (range - w * 32 < 32) lead &= (1u << (range - w * 32)) - 1u;
@@ -386,95 +482,25 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(AppendArgs a, in
       const int i = w * 32 + __ffs(lead) - 1;
       lead &= lead - 1u;
       const int n = run_length(i);
-      if (n <= kShortRun) {   // one warp for the keys, one for the values, in turn
+      if (S::kTeam > 1 && n <= kShortRun) {
 #pragma unroll 1
-        for (int half = 0; half < 2; ++half, ++n_short) {
-          if ((n_short & (kWords - 1)) != warp) continue;
-          const int slot = a.slots[r0 + i], off = slot % BS;
-          const size_t unit = ((size_t)(slot / BS) * a.Hkv + h) * 2 + half;
-          const Tin* src = static_cast<const Tin*>(half ? a.v : a.k) + (size_t)(r0 + i) * (half ? a.vstride : a.kstride) +
-                           (size_t)h * D;
-          const long stride = half ? a.vstride : a.kstride;
-          constexpr int kRows = 32 / kVecRow;                       // rows of one warp load
-          constexpr int kLoads = (kShortRun + kRows - 1) / kRows;
-          Eight<Tin> e[kLoads];
-          const float old = off ? a.scales[unit] : 0.f;
-          uint32_t m = 0u;
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const int row = l * kRows + lane / kVecRow;
-            e[l].zero();
-            if (row < n) e[l].load(src + (size_t)row * stride + (lane % kVecRow) * 8);
-          }
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            float x[8];
-            e[l].get(x);
-            m = max(m, amax8(x));
-          }
-          m = __reduce_max_sync(0xffffffffu, m);
-          float after = scale_for<T>(__uint_as_float(m));
-          if (off) after = fmaxf(after, old);
-          uint8_t* dst = a.cache + unit * (size_t)(BS * D);
-          if (off && after > old) requantise<T, D>(dst, off, old, after, lane, 32);
-          if (lane == 0 && (!off || after > old)) a.scales[unit] = after;
-          const bool pow2 = (__float_as_uint(after) & 0x7FFFFFu) == 0u;
-          const float inv = 1.f / after;
-#pragma unroll
-          for (int l = 0; l < kLoads; ++l) {
-            const int row = l * kRows + lane / kVecRow;
-            float x[8];
-            e[l].get(x);
-            if (row < n)
-              *reinterpret_cast<uint2*>(dst + (size_t)(off + row) * D + (lane % kVecRow) * 8) =
-                  quantise8<T>(x, after, inv, pow2);
-          }
+        for (int j = 0; j < 2 * S::kHeads; ++j, ++n_short) {
+          const int hj = blockIdx.y * S::kHeads + (j >> 1);
+          if ((n_short & (kWarps - 1)) == warp && hj < a.Hkv)
+            take(integral_constant<int, (kShortRun * S::kRowLanes + 31) / 32>{}, integral_constant<int, 1>{}, i, n, hj, j & 1, lane, in_warp);
         }
-        continue;
-      }
-      // the whole CTA
-      const int half = tid / kHalf, t = tid % kHalf;
-      const int slot = a.slots[r0 + i], off = slot % BS;
-      const size_t unit = ((size_t)(slot / BS) * a.Hkv + h) * 2 + half;
-      const long stride = half ? a.vstride : a.kstride;
-      const Tin* src = static_cast<const Tin*>(half ? a.v : a.k) + (size_t)(r0 + i) * stride + (size_t)h * D;
-      Eight<Tin> e[kPieces];
-      const float old = off ? a.scales[unit] : 0.f;
+      } else if (S::kTeam == 1) {
+        if (h < a.Hkv) take(integral_constant<int, S::kPieces>{}, integral_constant<int, 1>{}, i, n, h, half, t, in_warp);
+      } else if (h < a.Hkv) {
+        take(integral_constant<int, S::kPieces>{}, integral_constant<int, S::kTeam>{}, i, n, h, half, t, [&](uint32_t m) {
+          uint32_t* mine = s_max[n_long++ & 1];   // (two in turn: one barrier for each)
+          if (lane == 0) mine[warp] = m;
+          asm volatile("bar.sync %0, %1;" ::"r"(team + 1), "n"(S::kTeam * 32) : "memory");
+          m = 0u;
 #pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        const int idx = p * kHalf + t, row = idx / kVecRow;
-        e[p].zero();
-        if (row < n) e[p].load(src + (size_t)row * stride + (idx % kVecRow) * 8);
-      }
-      uint32_t m = 0u;
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        float x[8];
-        e[p].get(x);
-        m = max(m, amax8(x));
-      }
-      m = __reduce_max_sync(0xffffffffu, m);
-      __syncthreads();   // s_max is free again
-      if (lane == 0) s_max[warp] = m;
-      __syncthreads();   // (and every thread has read the old scale)
-      m = 0u;
-#pragma unroll
-      for (int x = 0; x < kWords / 2; ++x) m = max(m, s_max[half * (kWords / 2) + x]);
-      float after = scale_for<T>(__uint_as_float(m));
-      if (off) after = fmaxf(after, old);
-      uint8_t* dst = a.cache + unit * (size_t)(BS * D);
-      if (off && after > old) requantise<T, D>(dst, off, old, after, t, kHalf);
-      if (t == 0 && (!off || after > old)) a.scales[unit] = after;
-      const bool pow2 = (__float_as_uint(after) & 0x7FFFFFu) == 0u;
-      const float inv = 1.f / after;
-#pragma unroll
-      for (int p = 0; p < kPieces; ++p) {
-        const int idx = p * kHalf + t, row = idx / kVecRow;
-        float x[8];
-        e[p].get(x);
-        if (row < n)
-          *reinterpret_cast<uint2*>(dst + (size_t)(off + row) * D + (idx % kVecRow) * 8) =
-              quantise8<T>(x, after, inv, pow2);
+          for (int x = 0; x < S::kTeam; ++x) m = max(m, mine[team * S::kTeam + x]);
+          return m;
+        });
       }
     }
   }

@@ -148,7 +148,7 @@ def _expect(t, name, shape, dtype):
     output buffer is an error instead of an out-of-bounds write."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
@@ -428,32 +428,20 @@ def _kv_dt(cache: torch.Tensor) -> int:
     raise TypeError(f"unsupported cache dtype {cache.dtype} (float8_e4m3fn or int8)")
 
 
-class _On:
-    """The device and stream of a call: launches go to `dev` whatever device is current, and what
-    a call allocates belongs to the stream it runs on."""
-    __slots__ = ("dev", "stream", "_inner")
+def _elsewhere(dev, stream):
+    """What a call enters first if it runs on another stream than the current one, or on another device than the
+    current one (launches go to the tensors' device, and what a call allocates belongs to the stream it runs
+    on); None if nothing is to be entered."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+        return torch.cuda.stream(stream)   # (makes dev current as well)
+    return None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
-    def __init__(self, dev, stream):
-        self._inner = None
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-            if torch.cuda.current_device() != dev.index:
-                self._inner = torch.cuda.device(dev)
-        else:
-            if stream.device != dev:
-                raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-            self._inner = torch.cuda.stream(stream)   # (makes dev current as well)
-        self.stream = ctypes.c_void_p(stream.cuda_stream)
 
-    def __enter__(self):
-        if self._inner is not None:
-            self._inner.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._inner is not None:
-            self._inner.__exit__(*exc)
-        return False
+def _current_raw_stream(dev) -> int:
+    # (torch.cuda.current_stream() costs two microseconds, a third of a launch)
+    return torch._C._cuda_getCurrentRawStream(dev.index)
 
 
 def _need_cuda_strided(*ts):
@@ -535,19 +523,23 @@ def kv_cache_assign(new_lens, seq_lens, block_table, free_blocks, free_span, blo
     _expect(free_span_out, "free_span_out", (2,), i32)
     _need_cuda(new_lens, seq_lens, block_table, free_blocks, free_span, slot_map, cu_new, seq_lens_out, free_span_out)
     dev = new_lens.device
-    with _On(dev, stream) as s:
-        if slot_map is None:
-            slot_map = torch.empty(n_slots, device=dev, dtype=i32)
-        if cu_new is None:
-            cu_new = torch.empty(B + 1, device=dev, dtype=i32)
-        if seq_lens_out is None:
-            seq_lens_out = torch.empty(B, device=dev, dtype=i32)
-        if free_span_out is None:
-            free_span_out = torch.empty(2, device=dev, dtype=i32)
-        st = lib.liger_kv_cache_assign(
-            new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(), free_span.data_ptr(),
-            slot_map.data_ptr(), cu_new.data_ptr(), seq_lens_out.data_ptr(), free_span_out.data_ptr(), B, width, n_blocks,
-            block_size, n_slots, s)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return kv_cache_assign(new_lens, seq_lens, block_table, free_blocks, free_span, block_size, n_slots, slot_map,
+                                   cu_new, seq_lens_out, free_span_out)
+    if slot_map is None:
+        slot_map = new_lens.new_empty(n_slots)
+    if cu_new is None:
+        cu_new = new_lens.new_empty(B + 1)
+    if seq_lens_out is None:
+        seq_lens_out = torch.empty_like(seq_lens)
+    if free_span_out is None:
+        free_span_out = torch.empty_like(free_span)
+    st = lib.liger_kv_cache_assign(
+        new_lens.data_ptr(), seq_lens.data_ptr(), block_table.data_ptr(), free_blocks.data_ptr(), free_span.data_ptr(),
+        slot_map.data_ptr(), cu_new.data_ptr(), seq_lens_out.data_ptr(), free_span_out.data_ptr(), B, width, n_blocks,
+        block_size, n_slots, _current_raw_stream(dev))
     _check(st)
     return slot_map, cu_new, seq_lens_out, free_span_out
 
@@ -572,9 +564,12 @@ def kv_cache_append(k, v, slot_map, cache, scales, stream=None):
     dt = _dt(k)
     ks, vs = _token_stride(k, "k", Hkv, d), _token_stride(v, "v", Hkv, d)
     _need_cuda_strided(k, v, slot_map, cache, scales)
-    with _On(k.device, stream) as s:
-        st = lib.liger_kv_cache_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache.data_ptr(), scales.data_ptr(),
-                                       N, Hkv, d, n_blocks, block_size, ks, vs, dt, kv_dt, s)
+    on = _elsewhere(k.device, stream)
+    if on is not None:
+        with on:
+            return kv_cache_append(k, v, slot_map, cache, scales)
+    st = lib.liger_kv_cache_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache.data_ptr(), scales.data_ptr(),
+                                   N, Hkv, d, n_blocks, block_size, ks, vs, dt, kv_dt, _current_raw_stream(k.device))
     _check(st)
 
 
@@ -610,15 +605,18 @@ def cached_attention(q, cache, scales, block_table, seq_lens, out=None, workspac
             raise ValueError("block_table, seq_lens, out and workspace must be contiguous")
     dev = q.device
     _need_cuda_strided(q, cache, scales, block_table, seq_lens, *(t for t in (out, workspace) if t is not None))
-    with _On(dev, stream) as s:
-        if out is None:
-            out = torch.empty(q.shape, device=dev, dtype=q.dtype)
-        if workspace is None:
-            workspace = torch.empty(lib.liger_attn_cached_workspace_size(d), device=dev, dtype=torch.uint8)
-        st = lib.liger_attn_cached(
-            q.data_ptr(), cache.data_ptr(), scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
-            B, n_q, Hq, Hkv, d, width, n_blocks, block_size, qs, dt, kv_dt, workspace.data_ptr(),
-            workspace.numel() * workspace.element_size(), s)
+    on = _elsewhere(dev, stream)
+    if on is not None:
+        with on:
+            return cached_attention(q, cache, scales, block_table, seq_lens, out, workspace)
+    if out is None:
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if workspace is None:
+        workspace = torch.empty(lib.liger_attn_cached_workspace_size(d), device=dev, dtype=torch.uint8)
+    st = lib.liger_attn_cached(
+        q.data_ptr(), cache.data_ptr(), scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
+        B, n_q, Hq, Hkv, d, width, n_blocks, block_size, qs, dt, kv_dt, workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _current_raw_stream(dev))
     _check(st)
     return out
 
