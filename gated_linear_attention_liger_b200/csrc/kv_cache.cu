@@ -104,8 +104,7 @@ cudaError_t launch(void (*kern)(KArgs...), dim3 grid, unsigned block, size_t sme
 
 // ------------------------------------------------------------------ assign
 
-// Slots that one CTA writes along with everything else, in a single launch.  More go to many CTAs and a second
-// launch for the state.
+// Slots that one CTA writes along with everything else.  More go to many CTAs.
 constexpr int kOneCtaSlots = 16384;
 
 template <bool SLOTS, bool STATE>
@@ -215,6 +214,7 @@ liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_l
   if (st == LIGER_OK) st = check_sequences(B, table_width, block_size);
   if (st != LIGER_OK) return st;
   if (n_slots < 0) return fail(LIGER_ERR_INVALID_ARG, "need n_slots >= 0 (n_slots=%d)", n_slots);
+  if (n_slots > 0x7fffffff - 1024) return fail(LIGER_ERR_UNSUPPORTED, "too many slots (n_slots=%d)", n_slots);
   if (!new_lens || !seq_lens || !block_table || !free_blocks || !free_span || (n_slots && !slot_map) || !cu_new ||
       !seq_lens_out || !free_span_out)
     return fail(LIGER_ERR_INVALID_ARG, "all pointers must be non-null");
@@ -230,9 +230,14 @@ liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_l
     e = launch_assign<true, true>(a, 1, s);
   } else {
     const long long ctas = ((long long)n_slots + 4 * liger::kvc::kAssignThreads - 1) / (4 * liger::kvc::kAssignThreads);
-    const long long most = 4LL * liger::device_sm_count();
-    e = launch_assign<true, false>(a, (int)(ctas < most ? ctas : most), s);
-    if (e == cudaSuccess) e = launch_assign<false, true>(a, 1, s);
+    const long long most = 2LL * liger::device_sm_count();   // (they are all resident: each scans all sequences)
+    const int n = (int)(ctas < most ? ctas : most);
+    if (seq_lens_out != seq_lens && free_span_out != free_span) {
+      e = launch_assign<true, true>(a, n, s);
+    } else {   // every CTA reads the lengths and the span: they change when all have
+      e = launch_assign<true, false>(a, n, s);
+      if (e == cudaSuccess) e = launch_assign<false, true>(a, 1, s);
+    }
   }
   return e == cudaSuccess ? LIGER_OK : cuda_fail(e, "cache assignment launch");
 }

@@ -38,57 +38,61 @@ struct AssignArgs {
   int B, width, n_blocks, lbs, N;   // blocks of 2^lbs tokens
 };
 
-// Exclusive prefix sums over the block of two values; returns the block's totals in *ta, *tb.
-template <int THREADS>
-__device__ __forceinline__ void block_scan2(long long& a, long long& b, long long* ta, long long* tb,
-                                            long long (*part)[2]) {
+// Exclusive prefix sums over the block of K values; the block's totals in total[].
+template <int THREADS, int K>
+__device__ __forceinline__ void block_scan(long long (&v)[K], long long (&total)[K], long long (*part)[3]) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int W = THREADS / 32;
-  long long x = a, y = b;
+  long long x[K];
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-    if (lane >= o) { x += u; y += v; }
-  }
-  __syncthreads();   // part is free again
-  if (lane == 31) { part[warp][0] = x; part[warp][1] = y; }
-  __syncthreads();
-  if (warp == 0) {
-    long long u = lane < W ? part[lane][0] : 0, v = lane < W ? part[lane][1] : 0;
+  for (int k = 0; k < K; ++k) x[k] = v[k];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long p = __shfl_up_sync(0xffffffffu, u, o), q = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) { u += p; v += q; }
+  for (int o = 1; o < 32; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const long long u = __shfl_up_sync(0xffffffffu, x[k], o);
+      if (lane >= o) x[k] += u;
     }
-    if (lane < W) { part[lane][0] = u; part[lane][1] = v; }
-  }
+  __syncthreads();   // part is free again
+#pragma unroll
+  for (int k = 0; k < K; ++k)
+    if (lane == 31) part[warp][k] = x[k];
   __syncthreads();
-  a = x - a + (warp ? part[warp - 1][0] : 0);
-  b = y - b + (warp ? part[warp - 1][1] : 0);
-  *ta = part[W - 1][0];
-  *tb = part[W - 1][1];
+  // every warp scans the warps' sums for itself
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    long long p = lane < W ? part[lane][k] : 0;
+#pragma unroll
+    for (int o = 1; o < W; o <<= 1) {
+      const long long u = __shfl_up_sync(0xffffffffu, p, o);
+      if (lane >= o) p += u;
+    }
+    const long long before = __shfl_sync(0xffffffffu, p, warp ? warp - 1 : 0);
+    v[k] = x[k] - v[k] + (warp ? before : 0);
+    total[k] = __shfl_sync(0xffffffffu, p, W - 1);
+  }
 }
 
 constexpr int kAssignThreads = 512;
+constexpr int kTokenEach = 4;   // up to that many tokens a thread are taken one by one
 constexpr int kUnserved = -1;   // pre[] of a sequence that gets no slots
 
 inline size_t assign_smem_bytes(int B) { return sizeof(int32_t) * (4 * (size_t)B + 1); }
 
-// Every CTA scans all sequences (two block scans: tokens, then blocks taken and given back) and
-// takes its share of the rest: the slots of four consecutive tokens per thread, and a warp per
-// sequence for its table row and the blocks it gives back.  With SLOTS, it reads the tables and
+// Every CTA scans all sequences (one block scan of tokens, blocks taken and blocks given back; a second one only
+// where the slot map is too short) and takes its share of the rest: the slots of its threads' tokens, and a
+// warp per sequence for its table row and the blocks it gives back.  With SLOTS, it reads the tables and
 // the ring and writes slots, table and ring: blocks are taken from [head, head + taken) of the
 // ring and given back at [head + count, ...), which never overlap while the free blocks and
 // those in use are n_blocks in all, and only columns >= ceil(len / bs) of a table row are
 // written, which no slot reads (a new block's number is read from the ring).  So no CTA
-// depends on another.  With STATE (one CTA, the same launch or a later one), it writes the
-// offsets, lengths and span, which may stand where the inputs stand.
-// What bounds it: latency.  One CTA takes the lengths, two scans and one dependent table read in
-// a single launch; more tokens than kOneCtaSlots go to many CTAs and a second launch.
+// depends on another.  With STATE (the first CTA), it writes the offsets, lengths and span; where they stand in the
+// inputs' place, that is one CTA's work, in the same launch or in a later one.
+// What bounds it: latency.  The lengths, a scan and one dependent table or ring read.
 template <bool SLOTS, bool STATE>
-__global__ void __launch_bounds__(kAssignThreads) assign_kernel(AssignArgs a) {
+__global__ void __launch_bounds__(kAssignThreads, 2) assign_kernel(AssignArgs a) {
   extern __shared__ int32_t sm[];
-  __shared__ long long part[kAssignThreads / 32][2];
+  __shared__ long long part[kAssignThreads / 32][3];
   __shared__ int s_taken;
   int32_t* cu = sm;                  // [B + 1] token offsets, saturated
   int32_t* pre = cu + a.B + 1;       // [B] blocks taken before this sequence, or kUnserved
@@ -111,14 +115,21 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(AssignArgs a) {
     L = L < 0 ? 0 : (L > cap ? cap : L);
     const long long add = nw > 0 ? nw : 0;
     const long long have = (L + bs - 1) >> lbs;
-    long long toks = add, gone = in && nw < 0 ? have : 0, t1, t2;
-    block_scan2<kAssignThreads>(toks, gone, &t1, &t2, part);
-    const long long c0 = tok0 + toks, c1 = c0 + add;
-    const bool fits = in && nw >= 0 && L + add <= cap && c1 <= a.N;
-    const long long want = fits ? ((L + add + bs - 1) >> lbs) - have : 0;
-    long long need = want, unused = 0, t3, t4;
-    block_scan2<kAssignThreads>(need, unused, &t3, &t4, part);
-    need += need0;
+    const bool ends = in && nw < 0;
+    bool fits = in && nw >= 0 && L + add <= cap;
+    long long want = fits ? ((L + add + bs - 1) >> lbs) - have : 0;
+    long long v[3] = {add, ends ? have : 0, want}, total[3];
+    block_scan<kAssignThreads, 3>(v, total, part);
+    const long long c0 = tok0 + v[0], c1 = c0 + add;
+    if (tok0 + total[0] > a.N) {   // the slot map is too short for some
+      fits = fits && c1 <= a.N;
+      want = fits ? want : 0;
+      long long again[1] = {want}, sum[1];
+      block_scan<kAssignThreads, 1>(again, sum, part);
+      v[2] = again[0];
+      total[2] = sum[0];
+    }
+    const long long gone = v[1], need = need0 + v[2];
     const bool served = fits && (want == 0 || need + want <= count);
     // once one does not fit, none behind it that needs a block does: the served ones' blocks are the first
     if (served && want > 0) atomicMax(&s_taken, (int)(need + want));
@@ -127,16 +138,16 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(AssignArgs a) {
       pre[s] = served ? (int32_t)(need > n ? n : need) : kUnserved;   // above n only where no block is needed
       len[s] = (int32_t)L;
       back[s] = nw < 0 ? (int32_t)((back0 + gone) % n) : -1;
-      if (STATE) a.lens_out[s] = nw < 0 ? 0 : (int32_t)(L + (served ? add : 0));
+      if (STATE && blockIdx.x == 0) a.lens_out[s] = nw < 0 ? 0 : (int32_t)(L + (served ? add : 0));
     }
-    tok0 += t1;
-    back0 += t2;
-    need0 += t3;
+    tok0 += total[0];
+    back0 += total[1];
+    need0 += total[2];
   }
   if (threadIdx.x == 0) cu[0] = 0;
   __syncthreads();
   const int taken = s_taken;
-  if (STATE) {
+  if (STATE && blockIdx.x == 0) {
     for (int i = threadIdx.x; i <= a.B; i += kAssignThreads) a.cu[i] = cu[i];
     if (threadIdx.x == 0) {
       const long long left = (long long)count - taken + back0;
@@ -146,56 +157,111 @@ __global__ void __launch_bounds__(kAssignThreads) assign_kernel(AssignArgs a) {
   }
   if (!SLOTS) return;
 
-  // a sequence's new blocks into its row, an ended one's blocks back to the ring
+  // place i of the ring (n and the blocks of a row are below 2^27)
+  auto wrap = [&](int i) { return i < n ? i : (i < 2 * n ? i - n : i % n); };
+  // a sequence's new blocks into its row, an ended one's blocks back to the ring, eight a lane in flight
   const int warps = gridDim.x * (kAssignThreads / 32);
-  for (int s = blockIdx.x * (kAssignThreads / 32) + (threadIdx.x >> 5); s < a.B; s += warps) {
+  for (int s = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; s < a.B; s += warps) {
     const int lane = threadIdx.x & 31, have = (int)(((long long)len[s] + bs - 1) >> lbs);
     int32_t* row = a.table + (size_t)s * a.width;
-    if (back[s] >= 0) {
-      for (int j = lane; j < have; j += 32) a.ring[((long long)head + count + back[s] + j) % n] = row[j];
-    } else if (pre[s] != kUnserved) {
-      const long long end = (long long)len[s] + (cu[s + 1] - cu[s]);
-      const int upto = (int)((end + bs - 1) >> lbs);
-      for (int j = have + lane; j < upto; j += 32) row[j] = a.ring[((long long)head + pre[s] + j - have) % n];
+    const bool ended = back[s] >= 0;
+    if (!ended && pre[s] == kUnserved) continue;
+    const int upto = ended ? have : (int)(((long long)len[s] + (cu[s + 1] - cu[s]) + bs - 1) >> lbs);
+    const int at = ended ? wrap(wrap(head + count) + back[s]) : wrap(head + pre[s]);   // of the first one in the ring
+    const int from = ended ? 0 : have;
+    for (int j0 = from + lane; j0 < upto; j0 += 32 * 8) {
+      int32_t x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + 32 * e;
+        if (j < upto) x[e] = ended ? row[j] : a.ring[wrap(at + j - from)];
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int j = j0 + 32 * e;
+        if (j < upto) {
+          if (ended) a.ring[wrap(at + j - from)] = x[e];
+          else row[j] = x[e];
+        }
+      }
     }
   }
 
-  // slots, four tokens a thread
-  const int total = cu[a.B];
-  const long long quads = ((long long)a.N + 3) / 4;
-  const long long step = (long long)gridDim.x * kAssignThreads;
-  for (long long g = (long long)blockIdx.x * kAssignThreads + threadIdx.x; g < quads; g += step) {
-    const int i0 = (int)(4 * g);
-    int32_t out[4] = {-1, -1, -1, -1};
-    if (i0 < total) {
-      int lo = 0, hi = a.B;   // the last s with cu[s] <= i0
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cu[mid] <= i0) lo = mid;
-        else hi = mid;
-      }
-      int s = lo, blk = -1, id = -1;
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + e;
-        if (i >= total || i >= a.N) break;
-        while (cu[s + 1] <= i) { ++s; blk = -1; }
-        if (pre[s] == kUnserved) continue;
-        const int p = len[s] + (i - cu[s]);
-        const int b = p >> lbs;
-        if (b != blk) {
-          const int have = (int)(((long long)len[s] + bs - 1) >> lbs);
-          blk = b;
-          id = b < have ? a.table[(size_t)s * a.width + b] : a.ring[((long long)head + pre[s] + b - have) % n];
-          if (id < 0 || id >= n) id = -1;
-        }
-        out[e] = id < 0 ? -1 : (id << lbs) + (p & (bs - 1));
-      }
+  const int total = cu[a.B] < a.N ? cu[a.B] : a.N;
+  // the last sequence whose tokens begin at or before i
+  auto sequence_of = [&](int i) {
+    int lo = 0, hi = a.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cu[mid] <= i) lo = mid;
+      else hi = mid;
     }
-    if (a.N - i0 >= 4) {
-      *reinterpret_cast<int4*>(a.slots + i0) = make_int4(out[0], out[1], out[2], out[3]);
-    } else {
-      for (int e = 0; i0 + e < a.N; ++e) a.slots[i0 + e] = out[e];
+    return lo;
+  };
+  // where the number of block b of sequence s stands
+  auto place_of = [&](int s, int b) -> const int32_t* {
+    const int have = (int)(((long long)len[s] + bs - 1) >> lbs);
+    return b < have ? a.table + (size_t)s * a.width + b : a.ring + wrap(head + pre[s] + b - have);
+  };
+  auto slot_of = [&](int id, int p) { return id < 0 || id >= n ? -1 : (id << lbs) + (p & (bs - 1)); };
+  const int step = gridDim.x * kAssignThreads;
+  if (a.N <= kTokenEach * step) {   // few: a token a thread
+    for (int i = blockIdx.x * kAssignThreads + threadIdx.x; i < a.N; i += step) {
+      int slot = -1;
+      if (i < total) {
+        const int s = sequence_of(i);
+        if (pre[s] != kUnserved) {
+          const int p = len[s] + (i - cu[s]);
+          slot = slot_of(*place_of(s, p >> lbs), p);
+        }
+      }
+      a.slots[i] = slot;
+    }
+    return;
+  }
+  // Many: 512 consecutive tokens a warp.  Each lane looks up sixteen, which lie in one or two blocks of one sequence
+  // but at a sequence's end; then all lanes write them four by four, side by side.
+  const int lane = threadIdx.x & 31;
+  for (int c = blockIdx.x * (kAssignThreads / 32) + (threadIdx.x >> 5); c < (a.N + 511LL) / 512; c += step / 32) {
+    const int i0 = 512 * c + 16 * lane;
+    const int s0 = i0 < total ? sequence_of(i0) : 0;
+    const bool one = i0 < total && min(cu[s0 + 1], total) - i0 >= 16;
+    int id0 = -1, id1 = -1, p0 = 0;
+    if (one && pre[s0] != kUnserved) {
+      p0 = len[s0] + (i0 - cu[s0]);
+      id0 = *place_of(s0, p0 >> lbs);
+      id1 = *place_of(s0, (p0 + 15) >> lbs);
+    }
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int from = 8 * q + (lane >> 2), iq = 512 * c + 128 * q + 4 * lane;
+      const bool f_one = __shfl_sync(0xffffffffu, (int)one, from);
+      const int f_id0 = __shfl_sync(0xffffffffu, id0, from), f_id1 = __shfl_sync(0xffffffffu, id1, from);
+      const int f_p0 = __shfl_sync(0xffffffffu, p0, from);
+      int s = __shfl_sync(0xffffffffu, s0, from);
+      int out[4] = {-1, -1, -1, -1};
+      if (f_one) {
+        const int p = f_p0 + 4 * (lane & 3);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) out[e] = slot_of((p + e) >> lbs == f_p0 >> lbs ? f_id0 : f_id1, p + e);
+      } else if (iq < total) {
+#pragma unroll 1
+        for (int e = 0; e < 4 && iq + e < total; ++e) {
+          while (cu[s + 1] <= iq + e) ++s;
+          if (pre[s] != kUnserved) {
+            const int p = len[s] + (iq + e - cu[s]), slot = slot_of(*place_of(s, p >> lbs), p);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) out[x] = x == e ? slot : out[x];
+          }
+        }
+      }
+      if (a.N - iq >= 4) {
+        *reinterpret_cast<int4*>(a.slots + iq) = make_int4(out[0], out[1], out[2], out[3]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (e < a.N - iq) a.slots[iq + e] = out[e];
+      }
     }
   }
 }

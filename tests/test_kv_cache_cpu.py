@@ -52,7 +52,7 @@ INVALID, UNSUPPORTED = ops.LIGER_ERR_INVALID_ARG, ops.LIGER_ERR_UNSUPPORTED
     (dict(B=0), INVALID), (dict(width=0), INVALID), (dict(n=0), INVALID), (dict(bs=0), INVALID), (dict(N=-1), INVALID),
     (dict(new=None), INVALID), (dict(slots=None), INVALID), (dict(so=None), INVALID), (dict(slots=20), INVALID),
     (dict(lens=18), INVALID), (dict(bs=48), UNSUPPORTED), (dict(bs=256), UNSUPPORTED), (dict(B=8193), UNSUPPORTED),
-    (dict(n=1 << 27, bs=16), UNSUPPORTED), (dict(width=1 << 27, bs=16), UNSUPPORTED),
+    (dict(n=1 << 27, bs=16), UNSUPPORTED), (dict(width=1 << 27, bs=16), UNSUPPORTED), (dict(N=2 ** 31 - 1), UNSUPPORTED),
 ])
 def test_assign_rejects(lib, kw, status):
     assert _assign(lib, **kw) == status
