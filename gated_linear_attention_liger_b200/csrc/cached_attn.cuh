@@ -111,7 +111,7 @@ struct Smem {
 
 __device__ __forceinline__ void mma16816(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
@@ -167,16 +167,13 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 }
 
 // The line of work: sequence by sequence, unit by unit, a place for each tile and kUnitCost more behind a unit's last one
-// (its query operands and its output cost that much), cut into n equal stretches.  n is at most the line's length, so
-// that the tiles of one unit lie in consecutive stretches.
+// (its query operands and its output cost that much), cut into equal stretches of `per` places, one for each CTA.  The
+// tiles of one unit lie in consecutive stretches.
 constexpr int kUnitCost = 2;
 // a / b of numbers that are not negative, in 32 bits where they fit (the long division takes several times as long)
 __device__ __forceinline__ long long quotient(long long a, long long b) {
   return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
 }
-__device__ __forceinline__ long long cut(long long W, int c, int n) { return quotient(W * c, n); }
-// The stretch that holds place w.
-__device__ __forceinline__ int stretch_of(long long W, long long w, int n) { return (int)quotient((w + 1) * n - 1, W); }
 
 template <typename Tin, int D, KvType T, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -250,10 +247,13 @@ __global__ void __launch_bounds__(kThreads, 2)
   }
   const int units = a.Hkv * a.row_tiles;                     // of one sequence
   auto places = [&](int s) { return ((long long)first[s] + (long long)kUnitCost * before[s]) * units; };   // before sequence s
-  const long long W = places(a.B);
-  const int cta = blockIdx.x, n_cta = (int)(W < (long long)gridDim.x ? W : (long long)gridDim.x);
-  // tiles before place w of the line
-  auto tiles_before = [&](long long w) {
+  const long long W = places(a.B), per = quotient(W + gridDim.x - 1, gridDim.x);
+  const int cta = blockIdx.x;
+  // the tiles of this CTA's stretch: those before its first place and before its end, found by the even and the odd lanes
+  long long w0, w1;
+  int seq0;   // the sequence at the first place
+  {
+    const long long w = min(W, per * (cta + (lane & 1)));
     int lo = 0, hi = a.B;   // places(lo) <= w, and w < places(hi) but at the end
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -261,12 +261,15 @@ __global__ void __launch_bounds__(kThreads, 2)
       else hi = mid;
     }
     const int n = first[lo + 1] - first[lo];
-    if (n == 0) return (long long)first[lo] * units;
-    const long long r = w - places(lo), unit = quotient(r, n + kUnitCost), in = r - unit * (n + kUnitCost);
-    return (long long)first[lo] * units + (unit < units ? unit * n + (in < n ? in : n) : (long long)units * n);
-  };
-  // the tiles of this CTA's stretch
-  const long long w0 = cta < n_cta ? tiles_before(cut(W, cta, n_cta)) : 0, w1 = cta < n_cta ? tiles_before(cut(W, cta + 1, n_cta)) : 0;
+    long long t = (long long)first[lo] * units;
+    if (n > 0) {
+      const long long r = w - places(lo), unit = quotient(r, n + kUnitCost), in = r - unit * (n + kUnitCost);
+      t += unit < units ? unit * n + (in < n ? in : n) : (long long)units * n;
+    }
+    w0 = __shfl_sync(0xffffffffu, t, 0);
+    w1 = __shfl_sync(0xffffffffu, t, 1);
+    seq0 = __shfl_sync(0xffffffffu, lo, 0);
+  }
   const WaitCtx wc{abort_flag, a.err, a.wait_ns};
 
   const int bs = 1 << a.lbs, kLog = D == 128 ? 6 : 7, lbox = a.lbs < kLog ? a.lbs : kLog, box = 1 << lbox;   // rows of keys, and of values, of one copy
@@ -313,7 +316,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         it.vs = s.y;
       }
     };
-    Item cur = locate(w0, 0), next = locate(w0 + batch, cur.seq);
+    Item cur = locate(w0, seq0), next = locate(w0 + batch, cur.seq);
     fetch_scales(cur);
     int st = 0, issued = 0, turn = 0;   // the next stage, tiles issued (up to `stages`), uses of the stages
     bool ok = true;
@@ -365,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       };
       int t = 0;
       if (wb == w0)   // the first tiles' copies do not wait for their scales
-        for (; t < n_here && t < stages; ++t) issue(t, t);
+        for (; t < n_here && t < min(stages, 4); ++t) issue(t, t);
       ks = cur.id >= 0 ? cur.ks : 0.f;
       lv = __log2f(cur.vs);      // (both exact for a power of two)
       iv = __frcp_rn(cur.vs);
@@ -460,7 +463,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (!(u.flags & kEnds) && lane == 0) {   // the unit goes on in later stretches
         const int unit = u.head * a.row_tiles + u.row0 / kMaxRows;
         const long long w = places(u.seq) + (long long)unit * (u.tiles + kUnitCost);   // its first tile's place
-        a.split[cta] = make_int4(u.seq, unit, stretch_of(W, w, n_cta), stretch_of(W, w + u.tiles - 1, n_cta));
+        a.split[cta] = make_int4(u.seq, unit, (int)quotient(w, per), (int)quotient(w + u.tiles - 1, per));
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(parts_empty);
@@ -765,13 +768,12 @@ __global__ void __launch_bounds__(kThreads, 2)
 
 // Joins the units that lie in several stretches: the parts stand in the begin slot of the unit's first CTA and in the
 // continue slots of the others, and are added in a fixed order.  Each CTA whose stretch a unit goes on behind (all of the
-// unit's but the last) takes a share of the unit's output, 16 bytes a thread; up to kJoinLanes threads share the parts.
+// unit's but the last) takes a share of the unit's output; 16 bytes of it and a power of two of neighbouring lanes, which
+// share the parts.
 constexpr int kJoinThreads = 256;
 constexpr int kJoinLanes = 16;
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
-  __shared__ float4 s_x[kJoinThreads];
-  __shared__ float2 s_ml[kJoinThreads];
   const int tid = threadIdx.x;
   kvc::pdl_launch_next();
   kvc::pdl_wait_previous();
@@ -782,39 +784,37 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
   const int vecs = min(kMaxRows, a.rows - row0) * (D / 4);
   const int share = (vecs + parts - 2) / (parts - 1);              // of each of the unit's CTAs but the last
   const int v0 = ((int)blockIdx.x - c0) * share, v1 = min(vecs, v0 + share);
-  const int lanes = max(1, min(min(kJoinLanes, parts), kJoinThreads / share)), step = min(share, kJoinThreads);
-  const int e = tid / step;
-  for (int vb = v0; vb < v1; vb += step) {
-    const int v = vb + tid % step, r = v / (D / 4), c = v % (D / 4);
-    const bool in = v < v1 && e < lanes;
+  int log_lanes = 0;
+  while ((2 << log_lanes) <= min(kJoinLanes, parts) && (share << (log_lanes + 1)) <= kJoinThreads) ++log_lanes;
+  const int lanes = 1 << log_lanes, e = tid & (lanes - 1);
+  for (int vb = v0; vb < v1; vb += kJoinThreads >> log_lanes) {
+    const int v = vb + (tid >> log_lanes), r = v / (D / 4), c = v % (D / 4);
+    const bool in = v < v1;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = kNoRef, l = 0.f;
+    auto add = [&](float om, float ol, float4 y) {
+      const float top = fmaxf(m, om), f = ex2(m - top), g = ex2(om - top);
+      m = top;
+      l = l * f + ol * g;
+      x.x = x.x * f + y.x * g; x.y = x.y * f + y.y * g;
+      x.z = x.z * f + y.z * g; x.w = x.w * f + y.w * g;
+    };
     if (in)
 #pragma unroll 4
       for (int p = e; p < parts; p += lanes) {
         const int slot = p == 0 ? 2 * c0 + 1 : 2 * (c0 + p);
         const float* ml = a.part_ml + (size_t)slot * 2 * kMaxRows + r;
         const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((size_t)slot * kMaxRows + r) * D + 4 * c);
-        const float pm = ml[0], pl = ml[kMaxRows], top = fmaxf(m, pm), f = ex2(m - top), g = ex2(pm - top);
-        m = top;
-        l = l * f + pl * g;
-        x.x = x.x * f + y.x * g; x.y = x.y * f + y.y * g;
-        x.z = x.z * f + y.z * g; x.w = x.w * f + y.w * g;
+        add(ml[0], ml[kMaxRows], y);
       }
-    if (lanes > 1) {
-      s_x[tid] = x;
-      s_ml[tid] = make_float2(m, l);
-      __syncthreads();
-      if (in && e == 0)
-        for (int q = 1; q < lanes; ++q) {
-          const float4 y = s_x[q * step + tid];
-          const float2 o = s_ml[q * step + tid];
-          const float top = fmaxf(m, o.x), f = ex2(m - top), g = ex2(o.x - top);
-          m = top;
-          l = l * f + o.y * g;
-          x.x = x.x * f + y.x * g; x.y = x.y * f + y.y * g;
-          x.z = x.z * f + y.z * g; x.w = x.w * f + y.w * g;
-        }
+    for (int o = 1; o < lanes; o <<= 1) {
+      const float om = __shfl_xor_sync(0xffffffffu, m, o), ol = __shfl_xor_sync(0xffffffffu, l, o);
+      float4 y;
+      y.x = __shfl_xor_sync(0xffffffffu, x.x, o);
+      y.y = __shfl_xor_sync(0xffffffffu, x.y, o);
+      y.z = __shfl_xor_sync(0xffffffffu, x.z, o);
+      y.w = __shfl_xor_sync(0xffffffffu, x.w, o);
+      add(om, ol, y);
     }
     if (in && e == 0) {
       const float il = l == 0.f ? 0.f : 1.f / l;

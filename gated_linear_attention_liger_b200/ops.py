@@ -7,6 +7,7 @@ on first use; if it is missing this raises (there is no CPU fallback).
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 import threading
 from typing import Optional
@@ -77,6 +78,8 @@ class LigerError(RuntimeError):
 def load(path: Optional[str] = None):
     """Load the CUDA library (raises FileNotFoundError if it has not been built)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             p = path or LIB_PATH
@@ -445,13 +448,14 @@ def _current_raw_stream(dev) -> int:
 
 
 def _need_cuda_strided(*ts):
-    """As _need_cuda, for tensors whose layout has been checked apart."""
-    ref = ts[0].device
+    """As _need_cuda, for tensors whose layout has been checked apart.  Returns their device."""
+    at = ts[0].get_device()   # (-1 on the host)
     for t in ts:
-        if not t.is_cuda:
-            raise ValueError("tensors must be CUDA tensors")
-        if t.device != ref:
-            raise ValueError(f"tensors must be on one device ({ref} and {t.device})")
+        if t is not None and (at < 0 or t.get_device() != at):
+            if not t.is_cuda:
+                raise ValueError("tensors must be CUDA tensors")
+            raise ValueError(f"tensors must be on one device ({ts[0].device} and {t.device})")
+    return ts[0].device
 
 
 def _token_stride(t, name, heads, d):
@@ -521,17 +525,20 @@ def kv_cache_assign(new_lens, seq_lens, block_table, free_blocks, free_span, blo
     _expect(cu_new, "cu_new", (B + 1,), i32)
     _expect(seq_lens_out, "seq_lens_out", (B,), i32)
     _expect(free_span_out, "free_span_out", (2,), i32)
-    _need_cuda(new_lens, seq_lens, block_table, free_blocks, free_span, slot_map, cu_new, seq_lens_out, free_span_out)
-    dev = new_lens.device
+    tensors = (new_lens, seq_lens, block_table, free_blocks, free_span, slot_map, cu_new, seq_lens_out, free_span_out)
+    for t in tensors:
+        if t is not None and not t.is_contiguous():
+            raise ValueError("tensors must be contiguous CUDA tensors")
+    dev = _need_cuda_strided(*tensors)
     on = _elsewhere(dev, stream)
     if on is not None:
         with on:
             return kv_cache_assign(new_lens, seq_lens, block_table, free_blocks, free_span, block_size, n_slots, slot_map,
                                    cu_new, seq_lens_out, free_span_out)
     if slot_map is None:
-        slot_map = new_lens.new_empty(n_slots)
+        slot_map = torch.empty(n_slots, device=dev, dtype=i32)
     if cu_new is None:
-        cu_new = new_lens.new_empty(B + 1)
+        cu_new = torch.empty(B + 1, device=dev, dtype=i32)
     if seq_lens_out is None:
         seq_lens_out = torch.empty_like(seq_lens)
     if free_span_out is None:
@@ -563,18 +570,24 @@ def kv_cache_append(k, v, slot_map, cache, scales, stream=None):
         raise ValueError("slot_map must be contiguous")
     dt = _dt(k)
     ks, vs = _token_stride(k, "k", Hkv, d), _token_stride(v, "v", Hkv, d)
-    _need_cuda_strided(k, v, slot_map, cache, scales)
-    on = _elsewhere(k.device, stream)
+    dev = _need_cuda_strided(k, v, slot_map, cache, scales)
+    on = _elsewhere(dev, stream)
     if on is not None:
         with on:
             return kv_cache_append(k, v, slot_map, cache, scales)
     st = lib.liger_kv_cache_append(k.data_ptr(), v.data_ptr(), slot_map.data_ptr(), cache.data_ptr(), scales.data_ptr(),
-                                   N, Hkv, d, n_blocks, block_size, ks, vs, dt, kv_dt, _current_raw_stream(k.device))
+                                   N, Hkv, d, n_blocks, block_size, ks, vs, dt, kv_dt, _current_raw_stream(dev))
     _check(st)
 
 
 def cached_attention_workspace_size(d: int) -> int:
+    """Bytes of workspace of cached_attention on the current device."""
     return int(load().liger_attn_cached_workspace_size(d))
+
+
+@functools.lru_cache(maxsize=None)
+def _cached_workspace(device: int, d: int) -> int:
+    return cached_attention_workspace_size(d)
 
 
 def cached_attention(q, cache, scales, block_table, seq_lens, out=None, workspace=None, stream=None):
@@ -588,23 +601,23 @@ def cached_attention(q, cache, scales, block_table, seq_lens, out=None, workspac
     """
     lib = load()
     n_blocks, Hkv, block_size, d, kv_dt = _check_cache(cache, scales)
-    if q.dim() not in (3, 4) or q.shape[-1] != d:
+    shape = q.shape
+    if len(shape) not in (3, 4) or shape[-1] != d:
         raise ValueError(f"q must be [B, Hq, {d}] or [B, n_q, Hq, {d}]")
     if block_table.dim() != 2 or block_table.dtype != torch.int32:
         raise ValueError("block_table must be [B, width] int32")
-    B, Hq = q.shape[0], q.shape[-2]
-    n_q = q.shape[1] if q.dim() == 4 else 1
+    B, Hq = shape[0], shape[-2]
+    n_q = shape[1] if len(shape) == 4 else 1
     width = block_table.shape[1]
     _expect(block_table, "block_table", (B, width), torch.int32)
     _expect(seq_lens, "seq_lens", (B,), torch.int32)
-    _expect(out, "out", q.shape, q.dtype)
+    _expect(out, "out", shape, q.dtype)
     dt = _dt(q)
     qs = _token_stride(q, "q", Hq, d)
-    for t in (block_table, seq_lens, out, workspace):
-        if t is not None and not t.is_contiguous():
-            raise ValueError("block_table, seq_lens, out and workspace must be contiguous")
-    dev = q.device
-    _need_cuda_strided(q, cache, scales, block_table, seq_lens, *(t for t in (out, workspace) if t is not None))
+    if not (block_table.is_contiguous() and seq_lens.is_contiguous() and (out is None or out.is_contiguous())
+            and (workspace is None or workspace.is_contiguous())):
+        raise ValueError("block_table, seq_lens, out and workspace must be contiguous")
+    dev = _need_cuda_strided(q, cache, scales, block_table, seq_lens, out, workspace)
     on = _elsewhere(dev, stream)
     if on is not None:
         with on:
@@ -612,7 +625,7 @@ def cached_attention(q, cache, scales, block_table, seq_lens, out=None, workspac
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
-        workspace = torch.empty(lib.liger_attn_cached_workspace_size(d), device=dev, dtype=torch.uint8)
+        workspace = torch.empty(_cached_workspace(dev.index, d), device=dev, dtype=torch.uint8)
     st = lib.liger_attn_cached(
         q.data_ptr(), cache.data_ptr(), scales.data_ptr(), block_table.data_ptr(), seq_lens.data_ptr(), out.data_ptr(),
         B, n_q, Hq, Hkv, d, width, n_blocks, block_size, qs, dt, kv_dt, workspace.data_ptr(),
