@@ -55,10 +55,33 @@ using kvc::kInt8;
 
 constexpr int kWarps = 4;              // consumer warps
 constexpr int kThreads = 32 * (kWarps + 2);   // and the producer's and the output's warp
+constexpr int kEarly = 4;              // tiles that a stretch starts with before their scales have come
+constexpr int kJoinThreads = 256;
+constexpr int kJoinLanes = 16;        // at most, for a piece of a joined unit
 constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
 constexpr float kRefBelow = 7.f;       // the reference is set this far below the maximum,
 constexpr float kRaiseAt = 15.f;       // and raised when a score exceeds it by this much
 
+// Division of 0 .. 2^31 - 1 by a number known on the host: n m / 2^(31 + s), m the next integer above 2^(31 + s) / d, with
+// 2^s >= d.  (A division on the device takes some 300 cycles, and several stood one behind the other before the first copy.)
+struct Divisor {
+  uint32_t m;
+  int s, d;
+  static Divisor of(int d) {
+    Divisor x{0u, 0, d};
+    while ((1LL << x.s) < d) ++x.s;
+    x.m = (uint32_t)((1ULL << (31 + x.s)) / d + 1);
+    return x;
+  }
+  __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
+  __device__ __forceinline__ long long of_long(long long n) const { return n >> 31 ? n / d : (*this)((int)n); }
+};
+// A unit that several CTAs have parts of, as each of them but the last notes it down for the join.
+struct Split {
+  int seq, head, row0, n_rows;         // seq -1: none
+  int c0, parts;                       // the unit's first CTA, and how many it has
+  int share, log_lanes;                // 16-byte pieces of the output for each of those CTAs; lanes for each piece, as a power of two
+};
 struct Args {
   const void* q;            // [B, n_q, Hq, d], tokens qstride elements apart
   const float* scales;      // [n_blocks, Hkv, 2]
@@ -67,23 +90,25 @@ struct Args {
   void* out;                // [B, n_q, Hq, d]
   float* part_ml;           // [2 ctas][2][kMaxRows] references and sums of the parts
   float* part_o;            // [2 ctas][kMaxRows][d]
-  int4* split;              // [ctas] the unit that goes on behind a CTA's stretch: (sequence or -1, unit, first CTA, last CTA)
+  Split* split;             // [ctas] the unit that goes on behind a CTA's stretch
   uint32_t* err;
   uint64_t wait_ns;
   long qstride;
   float scale_log2;         // log2(e) / sqrt(d)
   int B, n_q, Hq, Hkv, G, width, n_blocks, lbs;   // blocks of 2^lbs tokens
   int rows, row_tiles;                            // rows = n_q * G
+  Divisor by_ctas, by_units, by_row_tiles, by_G;  // units = Hkv * row_tiles
 };
 constexpr int kMaxRows = 16;           // query rows of a unit
 
 struct StageInfo {
   int seq, head, row0, tok0;           // kv head, first query row, first cached token
   int len, flags;                      // tokens of the sequence; kFirst | kLast | kBegins | kEnds
-  int tiles, pad;                      // tiles of the unit
+  int pad0, pad1;
   float ks[8], lv[8], iv[8];           // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
 };
-enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8 };   // the first, last tile of this CTA's stretch of the unit / of the unit itself
+// the first, last tile of this CTA's stretch of the unit / of the unit itself; the stretch's last tile; no tile at all
+enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8, kFinal = 16, kNone = 32 };
 
 // Cached tokens of a tile: 16 KB of keys and values, whatever d, since a tile costs the producer and each consumer warp
 // about 1000 cycles besides its bytes.
@@ -92,7 +117,6 @@ constexpr int tile_tokens(int d) { return 8192 / d; }
 // What the consumer warps tell the output's warp about the unit that they have just ended.
 struct UnitInfo {
   int seq, head, row0, flags;
-  int tiles, k, pad0, pad1;            // the unit's tiles; the last one's number in the stretch
 };
 
 // Shared memory.  NT: query rows in eights (1 or 2).
@@ -197,8 +221,8 @@ __global__ void __launch_bounds__(kThreads, 2)
   float* red_ml = red + kWarps * part_rows * D;                       // [kWarps][part_rows][2]
   float* wgt = red_ml + kWarps * part_rows * 2;                       // [part_rows][kWarps]
   int* first = reinterpret_cast<int*>(part + 20) + (S::red(a.rows) + 15) / 16 * 4;   // [B + 1] tiles before each sequence
-  int* before = first + a.B + 1;                                      // [B + 1] sequences with tokens before each one
-  int* lens = before + a.B + 1;                                       // [B]
+  int* line = first + a.B + 1;                                        // [B + 1] places before each sequence, for one unit
+  int* lens = line + a.B + 1;                                         // [B]
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
@@ -238,38 +262,15 @@ __global__ void __launch_bounds__(kThreads, 2)
     for (int s = s0; s < s1; ++s) {
       const int n = (int)(((long long)lens[s] + kTile - 1) / kTile);
       first[s] = run;
-      before[s] = seqs;
+      line[s] = run + kUnitCost * seqs;
       run += n;
       seqs += n > 0;
     }
-    if (s1 == a.B && s0 < a.B) { first[a.B] = run; before[a.B] = seqs; }
+    if (s1 == a.B && s0 < a.B) { first[a.B] = run; line[a.B] = run + kUnitCost * seqs; }
     __syncthreads();
   }
   const int units = a.Hkv * a.row_tiles;                     // of one sequence
-  auto places = [&](int s) { return ((long long)first[s] + (long long)kUnitCost * before[s]) * units; };   // before sequence s
-  const long long W = places(a.B), per = quotient(W + gridDim.x - 1, gridDim.x);
   const int cta = blockIdx.x;
-  // the tiles of this CTA's stretch: those before its first place and before its end, found by the even and the odd lanes
-  long long w0, w1;
-  int seq0;   // the sequence at the first place
-  {
-    const long long w = min(W, per * (cta + (lane & 1)));
-    int lo = 0, hi = a.B;   // places(lo) <= w, and w < places(hi) but at the end
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (places(mid) <= w) lo = mid;
-      else hi = mid;
-    }
-    const int n = first[lo + 1] - first[lo];
-    long long t = (long long)first[lo] * units;
-    if (n > 0) {
-      const long long r = w - places(lo), unit = quotient(r, n + kUnitCost), in = r - unit * (n + kUnitCost);
-      t += unit < units ? unit * n + (in < n ? in : n) : (long long)units * n;
-    }
-    w0 = __shfl_sync(0xffffffffu, t, 0);
-    w1 = __shfl_sync(0xffffffffu, t, 1);
-    seq0 = __shfl_sync(0xffffffffu, lo, 0);
-  }
   const WaitCtx wc{abort_flag, a.err, a.wait_ns};
 
   const int bs = 1 << a.lbs, kLog = D == 128 ? 6 : 7, lbox = a.lbs < kLog ? a.lbs : kLog, box = 1 << lbox;   // rows of keys, and of values, of one copy
@@ -278,33 +279,46 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int lppt = kLog - lbox;                       // 2^lppt blocks of a tile
     const int batch = 32 >> lppt;                    // tiles looked up at once, a lane per block
     const int in_tile = lane & ((1 << lppt) - 1), lane_tile = lane >> lppt;
-    struct Item { int seq, head, row0, tile, tiles, id; float ks, vs; };
-    // The lane's block of the batch that starts at w: its place in the line, then its number (`id`, as the table
+    // this CTA's stretch of the line
+    const long long W = (long long)line[a.B] * units, per = a.by_ctas.of_long(W + gridDim.x - 1);
+    const long long p0 = min(W, per * cta), p1 = min(W, per * (cta + 1));
+    // the last sequence whose places begin at or before p0, 32 probes at a time
+    int seq0 = 0;
+    for (int n = a.B, f = (int)a.by_units.of_long(p0); n > 1;) {
+      const int step = (n + 31) >> 5;
+      const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && line[min(seq0 + lane * step, a.B)] <= f);
+      const int hit = 31 - __clz(below);   // (the first probe always is)
+      n = min(step, n - hit * step);
+      seq0 += hit * step;
+    }
+    struct Item { int seq, head, row0, tile, tiles, id; float ks, vs; };   // tile < tiles where there is one
+    // The lane's block of the batch of places that starts at p: where it belongs, then its number (`id`, as the table
     // has it), then its scales.  Each step's load is used a batch later, so none is waited for but the first.
-    auto locate = [&](long long w, int lo) {
+    auto locate = [&](long long p, int lo) {
       Item it{lo, 0, 0, 0, 0, -1, 0.f, 1.f};
-      w += lane_tile;
-      if (w < w1) {
-        if ((long long)first[lo + 1] * units <= w) {
-          int hi = a.B;   // first[lo] * units <= w < first[hi] * units
+      p += lane_tile;
+      if (p < p1) {
+        for (int near = 0; near < 4 && (long long)line[lo + 1] * units <= p; ++near) ++lo;
+        if ((long long)line[lo + 1] * units <= p) {
+          int hi = a.B;   // line[lo] * units <= p < line[hi] * units
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if ((long long)first[mid] * units <= w) lo = mid;
+            if ((long long)line[mid] * units <= p) lo = mid;
             else hi = mid;
           }
         }
-        const long long r = w - (long long)first[lo] * units;
+        const long long r = p - (long long)line[lo] * units;
         it.seq = lo;
         it.tiles = first[lo + 1] - first[lo];
-        const int unit = (int)quotient(r, it.tiles);
-        it.tile = (int)(r - (long long)unit * it.tiles);
+        const int unit = (int)quotient(r, it.tiles + kUnitCost);
+        it.tile = (int)(r - (long long)unit * (it.tiles + kUnitCost));
         it.head = unit;
         if (a.row_tiles > 1) {
-          it.head = unit / a.row_tiles;
+          it.head = a.by_row_tiles(unit);
           it.row0 = (unit - it.head * a.row_tiles) * kMaxRows;
         }
         const long long tok = (long long)it.tile * kTile + in_tile * box;
-        if (tok < lens[lo]) it.id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
+        if (it.tile < it.tiles && tok < lens[lo]) it.id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
       }
       return it;
     };
@@ -316,16 +330,22 @@ __global__ void __launch_bounds__(kThreads, 2)
         it.vs = s.y;
       }
     };
-    Item cur = locate(w0, seq0), next = locate(w0 + batch, cur.seq);
+    Item cur = locate(p0, seq0), next = locate(p0 + batch, cur.seq);
     fetch_scales(cur);
     int st = 0, issued = 0, turn = 0;   // the next stage, tiles issued (up to `stages`), uses of the stages
-    bool ok = true;
-    for (long long wb = w0; wb < w1 && ok; wb += batch) {
-      const int n_here = (int)(w1 - wb < batch ? w1 - wb : batch);
-      const long long w = wb + lane_tile;
-      const bool opens = cur.tile == 0 || w == w0, ends = cur.tile == cur.tiles - 1;
-      const int flags = (opens ? kFirst : 0) | (ends || w == w1 - 1 ? kLast : 0) | (cur.tile == 0 ? kBegins : 0) | (ends ? kEnds : 0);
+    bool ok = true, any = false;
+    if (lane == 0) a.split[cta].seq = -1;   // (written again by the lane that finds a unit that goes on)
+    __syncwarp();
+    for (long long pb = p0; pb < p1 && ok; pb += batch) {
+      const long long p = pb + lane_tile;
+      const bool real = cur.tile < cur.tiles;
+      const bool opens = cur.tile == 0 || p == p0, ends = cur.tile == cur.tiles - 1;
+      const bool final = p + 1 + (ends ? kUnitCost : 0) >= p1;
+      const int flags = (opens ? kFirst : 0) | (ends || final ? kLast : 0) | (cur.tile == 0 ? kBegins : 0) | (ends ? kEnds : 0) |
+                        (final ? kFinal : 0);
       const uint32_t live = __ballot_sync(0xffffffffu, cur.id >= 0), opening = __ballot_sync(0xffffffffu, opens);
+      uint32_t todo = __ballot_sync(0xffffffffu, real && in_tile == 0);   // a bit for each tile, at its first lane
+      any = any || todo;
       const uint32_t blocks = (live >> (lane & ~((1 << lppt) - 1))) & ((1u << (1 << lppt)) - 1u);   // of the lane's tile
       const uint32_t bytes = __popc(blocks) * 2 * box * D + (opens ? min(kRows, a.rows - cur.row0) * D * (int)sizeof(Tin) : 0);
       // a tile's copies: keys and values of each block in one, and the query rows where a unit starts
@@ -340,7 +360,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if ((opening >> owner) & 1u) {   // rows are (token, head) pairs: one copy for each token's heads
           const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), head = __shfl_sync(0xffffffffu, cur.head, owner);
           const int r0 = __shfl_sync(0xffffffffu, cur.row0, owner), r1 = min(r0 + kRows, a.rows);
-          const int i = r0 / a.G + lane, lo = max(r0, i * a.G), hi = min(r1, (i + 1) * a.G);
+          const int i = a.by_G(r0) + lane, lo = max(r0, i * a.G), hi = min(r1, (i + 1) * a.G);
           if (lo < hi)
             bulk_load(dst + S::KV + (lo - r0) * D * sizeof(Tin),
                       static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(head * a.G + lo - i * a.G) * D,
@@ -360,36 +380,65 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
           if (in_tile == 0) {
             *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, cur.head, cur.row0, cur.tile * kTile);
-            *reinterpret_cast<int4*>(&si.len) = make_int4(lens[cur.seq], flags, cur.tiles, 0);
+            *reinterpret_cast<int4*>(&si.len) = make_int4(lens[cur.seq], flags, 0, 0);
           }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[at]);
       };
-      int t = 0;
-      if (wb == w0)   // the first tiles' copies do not wait for their scales
-        for (; t < n_here && t < min(stages, 4); ++t) issue(t, t);
+      auto next_tile = [&]() {
+        const int t = (__ffs(todo) - 1) >> lppt;
+        todo &= todo - 1u;
+        return t;
+      };
+      int early[kEarly], n_early = 0;
+      if (pb == p0)   // the first tiles' copies do not wait for their scales
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i)
+          if (todo && i < stages) {
+            early[i] = next_tile();
+            issue(early[i], i);
+            n_early = i + 1;
+          }
       ks = cur.id >= 0 ? cur.ks : 0.f;
       lv = __log2f(cur.vs);      // (both exact for a power of two)
       iv = __frcp_rn(cur.vs);
-      for (int i = 0; i < t; ++i) publish(i, i);
-      if (wb == w0) {
-        issued = t;
-        st = t == stages ? 0 : t;
-        turn = t == stages ? 1 : 0;
+      if (pb == p0) {
+#pragma unroll
+        for (int i = 0; i < kEarly; ++i)
+          if (i < n_early) publish(early[i], i);
+        issued = n_early;
+        st = n_early == stages ? 0 : n_early;
+        turn = n_early == stages ? 1 : 0;
       }
       fetch_scales(next);
-      const Item later = locate(wb + 2 * batch, next.seq);
-      for (; t < n_here; ++t) {
+      const Item later = locate(pb + 2 * batch, next.seq);
+      while (todo) {
         if (turn > 0) ok = warp_all(mbar_wait(&empty[st], (turn - 1) & 1, wc, wsite(1, st, turn)));
         if (!ok) break;
+        const int t = next_tile();
         issue(t, st);
         publish(t, st);
         issued = min(issued + 1, stages);
         if (++st == stages) { st = 0; ++turn; }
       }
+      // the unit that goes on behind this stretch, for the join
+      if (real && final && !ends && in_tile == 0) {
+        const int c0 = (int)quotient(p - cur.tile, per), parts = (int)quotient(p - cur.tile + cur.tiles - 1, per) - c0 + 1;
+        const int n_rows = min(kRows, a.rows - cur.row0), share = (n_rows * (D / 4) + parts - 2) / (parts - 1);
+        int log_lanes = 0;
+        while ((2 << log_lanes) <= min(kJoinLanes, parts) && (share << (log_lanes + 1)) <= kJoinThreads) ++log_lanes;
+        a.split[cta] = Split{cur.seq, cur.head, cur.row0, n_rows, c0, parts, share, log_lanes};
+      }
       cur = next;
       next = later;
+    }
+    if (!any) {   // an empty stretch, or two places behind a unit
+      if (lane == 0) {
+        info[0].flags = kNone;
+        mbar_arrive(&full[0]);
+      }
+      __syncwarp();
     }
     // never leave with copies in flight
     const WaitCtx dw{never, nullptr, a.wait_ns};
@@ -400,7 +449,6 @@ __global__ void __launch_bounds__(kThreads, 2)
     return;
   }
 
-  const int n_tiles = (int)(w1 - w0);
   if (warp == kWarps + 1) {   // ---------------- output
     // sequences without tokens: zero rows
     for (int s = cta; s < a.B; s += gridDim.x)
@@ -409,12 +457,11 @@ __global__ void __launch_bounds__(kThreads, 2)
         const int n16 = a.n_q * a.Hq * D * (int)sizeof(Tin) / 16;
         for (int i = lane; i < n16; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
       }
-    if (lane == 0) a.split[cta] = make_int4(-1, 0, 0, 0);   // (the same thread writes it again)
     // joins the four warps' parts of each unit's stretch
-    for (int done = 0, use = 0; done < n_tiles; ++use) {
-      if (!warp_all(mbar_wait(parts_full, use & 1, wc, wsite(4, 0, done)))) return;
+    for (int use = 0;; ++use) {
+      if (!warp_all(mbar_wait(parts_full, use & 1, wc, wsite(4, 0, use)))) return;
       const UnitInfo u = *unit_info;
-      done = u.k + 1;
+      if (u.flags & kNone) return;
       const int n_rows = min(kRows, a.rows - u.row0);
       const bool begins = u.flags & kBegins, whole = begins && (u.flags & kEnds);
       const int place = 2 * cta + (begins ? 1 : 0);   // of a part of a unit that goes on, or that an earlier CTA began
@@ -450,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         y.z = f.x * x0.z + f.y * x1.z + f.z * x2.z + f.w * x3.z;
         y.w = f.x * x0.w + f.y * x1.w + f.z * x2.w + f.w * x3.w;
         if (whole) {
-          const int row = u.row0 + r, i = row / a.G, h = u.head * a.G + row - i * a.G;
+          const int row = u.row0 + r, i = a.by_G(row), h = u.head * a.G + row - i * a.G;
           Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
           if (sizeof(Tin) == 2)
             *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(y.x, y.y), pack_bf16(y.z, y.w));
@@ -460,15 +507,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           *reinterpret_cast<float4*>(a.part_o + ((size_t)place * kMaxRows + r) * D + 4 * c) = y;
         }
       }
-      if (!(u.flags & kEnds) && lane == 0) {   // the unit goes on in later stretches
-        const int unit = u.head * a.row_tiles + u.row0 / kMaxRows;
-        const long long w = places(u.seq) + (long long)unit * (u.tiles + kUnitCost);   // its first tile's place
-        a.split[cta] = make_int4(u.seq, unit, (int)quotient(w, per), (int)quotient(w + u.tiles - 1, per));
-      }
+      if (u.flags & kFinal) return;
       __syncwarp();
       if (lane == 0) mbar_arrive(parts_empty);
     }
-    return;
   }
 
   // ---------------- consumers: a warp takes kSlices times 16 tokens of each tile
@@ -485,11 +527,18 @@ __global__ void __launch_bounds__(kThreads, 2)
   int row0 = 0;
   bool begins = false;                  // the CTA's stretch of the unit starts with its first tile
   uint32_t units_done = 0;
-  for (int k = 0, st = 0, phase = 0; k < n_tiles; ++k) {
+  for (int k = 0, st = 0, phase = 0;; ++k) {
     if (!warp_all(mbar_wait(&full[st], phase, wc, wsite(2, st, k)))) return;
     const StageInfo& si = info[st];
     const char* sk = smem + st * S::STAGE;
-    const int flags = si.flags, len = si.len, tok = si.tok0 + 16 * slot;
+    const int flags = si.flags;
+    if (flags & kNone) {
+      if (tid == 0) unit_info->flags = kNone;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(parts_full);
+      return;
+    }
+    const int len = si.len, tok = si.tok0 + 16 * slot;
     if (flags & kFirst) {
       row0 = si.row0;
       begins = (flags & kBegins) != 0;
@@ -538,7 +587,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         for (int c = 0; c < 2; ++c) {   // the thread's score columns are rows 2 t4 + c
           const int r = row0 + 8 * n + 2 * t4 + c;
           rs[n][c] = __shfl_sync(0xffffffffu, up, (2 * t4 + c) * 4) * a.scale_log2;
-          lim[n][c] = len - a.n_q + r / a.G + 1;
+          lim[n][c] = len - a.n_q + a.by_G(r) + 1;
           ref[n][c] = kNoRef;
           sum[n][c] = 0.f;
         }
@@ -733,7 +782,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           if (tok + 16 * u < len && si.ks[slot + u] != 0.f) slices(One{}, std::true_type{}, u, tok + 16 * u);
       }
     }
-    const UnitInfo u{si.seq, si.head, row0, (flags & kEnds) | (begins ? kBegins : 0), si.tiles, k, 0, 0};
+    const UnitInfo u{si.seq, si.head, row0, (flags & (kEnds | kFinal)) | (begins ? kBegins : 0)};
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
     if (++st == stages) { st = 0; phase ^= 1; }
@@ -763,6 +812,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       __syncwarp();
       if (lane == 0) mbar_arrive(parts_full);
     }
+    if (flags & kFinal) return;
   }
 }
 
@@ -770,25 +820,17 @@ __global__ void __launch_bounds__(kThreads, 2)
 // continue slots of the others, and are added in a fixed order.  Each CTA whose stretch a unit goes on behind (all of the
 // unit's but the last) takes a share of the unit's output; 16 bytes of it and a power of two of neighbouring lanes, which
 // share the parts.
-constexpr int kJoinThreads = 256;
-constexpr int kJoinLanes = 16;
 template <typename Tin, int D>
 __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
   const int tid = threadIdx.x;
   kvc::pdl_launch_next();
   kvc::pdl_wait_previous();
-  const int4 u = a.split[blockIdx.x];
-  if (u.x < 0) return;
-  const int head = u.y / a.row_tiles, row0 = (u.y - head * a.row_tiles) * kMaxRows;
-  const int c0 = u.z, parts = u.w - c0 + 1;
-  const int vecs = min(kMaxRows, a.rows - row0) * (D / 4);
-  const int share = (vecs + parts - 2) / (parts - 1);              // of each of the unit's CTAs but the last
-  const int v0 = ((int)blockIdx.x - c0) * share, v1 = min(vecs, v0 + share);
-  int log_lanes = 0;
-  while ((2 << log_lanes) <= min(kJoinLanes, parts) && (share << (log_lanes + 1)) <= kJoinThreads) ++log_lanes;
-  const int lanes = 1 << log_lanes, e = tid & (lanes - 1);
-  for (int vb = v0; vb < v1; vb += kJoinThreads >> log_lanes) {
-    const int v = vb + (tid >> log_lanes), r = v / (D / 4), c = v % (D / 4);
+  const Split u = a.split[blockIdx.x];
+  if (u.seq < 0) return;
+  const int v0 = ((int)blockIdx.x - u.c0) * u.share, v1 = min(u.n_rows * (D / 4), v0 + u.share);
+  const int lanes = 1 << u.log_lanes, e = tid & (lanes - 1);
+  for (int vb = v0; vb < v1; vb += kJoinThreads >> u.log_lanes) {
+    const int v = vb + (tid >> u.log_lanes), r = v / (D / 4), c = v % (D / 4);
     const bool in = v < v1;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = kNoRef, l = 0.f;
@@ -801,8 +843,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
     };
     if (in)
 #pragma unroll 4
-      for (int p = e; p < parts; p += lanes) {
-        const int slot = p == 0 ? 2 * c0 + 1 : 2 * (c0 + p);
+      for (int p = e; p < u.parts; p += lanes) {
+        const int slot = p == 0 ? 2 * u.c0 + 1 : 2 * (u.c0 + p);
         const float* ml = a.part_ml + (size_t)slot * 2 * kMaxRows + r;
         const float4 y = *reinterpret_cast<const float4*>(a.part_o + ((size_t)slot * kMaxRows + r) * D + 4 * c);
         add(ml[0], ml[kMaxRows], y);
@@ -818,8 +860,8 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
     }
     if (in && e == 0) {
       const float il = l == 0.f ? 0.f : 1.f / l;
-      const int row = row0 + r, i = row / a.G, h = head * a.G + row - i * a.G;
-      Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.x * a.n_q + i) * a.Hq + h) * D + 4 * c;
+      const int row = u.row0 + r, i = a.by_G(row), h = u.head * a.G + row - i * a.G;
+      Tin* dst = static_cast<Tin*>(a.out) + (((size_t)u.seq * a.n_q + i) * a.Hq + h) * D + 4 * c;
       if (sizeof(Tin) == 2)
         *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16(x.x * il, x.y * il), pack_bf16(x.z * il, x.w * il));
       else

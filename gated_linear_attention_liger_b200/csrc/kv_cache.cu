@@ -162,12 +162,12 @@ AttnLayout attn_layout(int d) {
   L.off_ml = 0;
   L.off_o = up(L.off_ml + (size_t)L.ctas * 2 * 2 * liger::ca::kMaxRows * 4);
   L.off_split = up(L.off_o + (size_t)L.ctas * 2 * liger::ca::kMaxRows * d * 4);
-  L.total = up(L.off_split + (size_t)L.ctas * 16);
+  L.total = up(L.off_split + (size_t)L.ctas * sizeof(liger::ca::Split));
   return L;
 }
 
 template <typename Tin, int D, KvType T, int NT>
-liger_status launch_attn(const CUtensorMap& tm, const liger::ca::Args& a, int ctas, cudaStream_t s) {
+liger_status launch_attn(const CUtensorMap& tm, liger::ca::Args a, int ctas, cudaStream_t s) {
   using S = liger::ca::Smem<Tin, D, NT>;
   // shared memory of one CTA with two on an SM (228 KB, 1 KB of it the system's, each), else alone
   constexpr int kShare = (228 * 1024) / kCtasPerSm - 1024, kAlone = 227 * 1024;
@@ -178,6 +178,7 @@ liger_status launch_attn(const CUtensorMap& tm, const liger::ca::Args& a, int ct
     ctas /= kCtasPerSm;
   }
   if (stages > S::MAX_STAGES) stages = S::MAX_STAGES;
+  a.by_ctas = liger::ca::Divisor::of(ctas);
   const int smem = (int)S::bytes(stages, a.rows, a.B);
   auto kern = liger::ca::cached_attn_kernel<Tin, D, T, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -294,7 +295,7 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
     return fail(LIGER_ERR_INVALID_ARG, "the query's token stride must be at least Hq * d elements and a multiple of 16 bytes");
   const int tile = liger::ca::tile_tokens(d);
   const long long tiles = (long long)B * (((long long)table_width * block_size + tile - 1) / tile);
-  if ((long long)n_blocks * Hkv > 0x7fffffffLL || tiles > 0x7fffffffLL)
+  if ((long long)n_blocks * Hkv > 0x7fffffffLL || tiles > 0x7fffffffLL - 65536)
     return fail(LIGER_ERR_UNSUPPORTED, "cache too large");
   if (!q || !cache || !scales || !block_table || !seq_lens || !out)
     return fail(LIGER_ERR_INVALID_ARG, "all pointers must be non-null");
@@ -332,7 +333,7 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   a.out = out;
   a.part_ml = reinterpret_cast<float*>(ws + L.off_ml);
   a.part_o = reinterpret_cast<float*>(ws + L.off_o);
-  a.split = reinterpret_cast<int4*>(ws + L.off_split);
+  a.split = reinterpret_cast<liger::ca::Split*>(ws + L.off_split);
   a.err = static_cast<uint32_t*>(err);
   a.wait_ns = liger::bounded_wait_ns();
   a.qstride = (long)q_stride;
@@ -347,6 +348,9 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   a.lbs = log2_block(block_size);
   a.rows = (int)rows;
   a.row_tiles = (int)((rows + liger::ca::kMaxRows - 1) / liger::ca::kMaxRows);
+  a.by_units = liger::ca::Divisor::of(Hkv * a.row_tiles);
+  a.by_row_tiles = liger::ca::Divisor::of(a.row_tiles);
+  a.by_G = liger::ca::Divisor::of(a.G);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   return dt == LIGER_BF16 ? attn_t<__nv_bfloat16>(tm, a, d, kv_dt, L.ctas, s) : attn_t<float>(tm, a, d, kv_dt, L.ctas, s);
 }
