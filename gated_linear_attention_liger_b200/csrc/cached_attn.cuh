@@ -105,7 +105,7 @@ struct StageInfo {
   int seq, head, row0, tok0;           // kv head, first query row, first cached token
   int len, flags;                      // tokens of the sequence; kFirst | kLast | kBegins | kEnds
   int pad0, pad1;
-  float ks[8], lv[8], iv[8];           // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
+  float4 scale[8];                     // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
 };
 // the first, last tile of this CTA's stretch of the unit / of the unit itself; the stretch's last tile; no tile at all
 enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8, kFinal = 16, kNone = 32 };
@@ -186,6 +186,15 @@ __device__ __forceinline__ uint32_t swz(int row, int byte) {
   return (uint32_t)(row * 64 + (byte ^ (((row >> 1) & 3) << 4)));
 }
 
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
 __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
@@ -372,12 +381,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       auto publish = [&](int t, int at) {
         StageInfo& si = info[at];
         if (lane_tile == t) {
-          for (int e = 0; e < box / 16; ++e) {
-            const int slot = in_tile * (box / 16) + e;
-            si.ks[slot] = ks;
-            si.lv[slot] = lv;
-            si.iv[slot] = iv;
-          }
+          for (int e = 0; e < box / 16; ++e) si.scale[in_tile * (box / 16) + e] = make_float4(ks, lv, iv, 0.f);
           if (in_tile == 0) {
             *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, cur.head, cur.row0, cur.tile * kTile);
             *reinterpret_cast<int4*>(&si.len) = make_int4(lens[cur.seq], flags, 0, 0);
@@ -527,20 +531,23 @@ __global__ void __launch_bounds__(kThreads, 2)
   int row0 = 0;
   bool begins = false;                  // the CTA's stretch of the unit starts with its first tile
   uint32_t units_done = 0;
+  bool ready = false;                   // the next tile had come when the last one was begun (a test's answer takes 100 cycles)
   for (int k = 0, st = 0, phase = 0;; ++k) {
-    if (!warp_all(mbar_wait(&full[st], phase, wc, wsite(2, st, k)))) return;
+    if (!warp_all(ready) && !warp_all(mbar_wait(&full[st], phase, wc, wsite(2, st, k)))) return;
     const StageInfo& si = info[st];
     const char* sk = smem + st * S::STAGE;
-    const int flags = si.flags;
+    const int4 where = *reinterpret_cast<const int4*>(&si.seq);   // sequence, head, first row, first token
+    const int2 what = *reinterpret_cast<const int2*>(&si.len);    // length, flags
+    const int flags = what.y;
     if (flags & kNone) {
       if (tid == 0) unit_info->flags = kNone;
       __syncwarp();
       if (lane == 0) mbar_arrive(parts_full);
       return;
     }
-    const int len = si.len, tok = si.tok0 + 16 * slot;
+    const int len = what.x, tok = where.w + 16 * slot;
     if (flags & kFirst) {
-      row0 = si.row0;
+      row0 = where.z;
       begins = (flags & kBegins) != 0;
       const char* sq = sk + S::KV;
 #pragma unroll
@@ -597,19 +604,25 @@ __global__ void __launch_bounds__(kThreads, 2)
           for (int c = 0; c < 4; ++c) o[n][i][c] = 0.f;
       }
     }
+    const int st_next = st + 1 == stages ? 0 : st + 1, phase_next = st_next ? phase : phase ^ 1;
+    ready = mbar_test(&full[st_next], phase_next);
     {
+      const float4* sc = si.scale + slot;
       // One or two slices of 16 tokens: `u` the first, its first token `at`.  At the sequence's end (at_end), or where a
       // slice has no block, they are taken one by one and masked.
       auto slices = [&](auto count, auto at_end, int u, int at) {
         constexpr int NS = decltype(count)::value;
         constexpr bool kEdge = decltype(at_end)::value;
-        float s[NS][NT][4];
+        constexpr int NA = NS * NT >= 4 ? 1 : 4 / (NS * NT);   // sums side by side: a product waits 30 cycles for the last one
+        float s[NS][NT][4], sa[NA][NS][NT][4];
 #pragma unroll
-        for (int i = 0; i < NS; ++i)
+        for (int x = 0; x < NA; ++x)
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int i = 0; i < NS; ++i)
 #pragma unroll
-            for (int c = 0; c < 4; ++c) s[i][n][c] = 0.f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int c = 0; c < 4; ++c) sa[x][i][n][c] = 0.f;
         {
           uint32_t kw[NS][2][KS];   // keys: rows g and g + 8 of the 16 tokens
 #pragma unroll
@@ -631,19 +644,43 @@ __global__ void __launch_bounds__(kThreads, 2)
               codes_to_f16<T>(kw[i][1][j], a1, a3);
 #pragma unroll
               for (int n = 0; n < NT; ++n) {
-                mma16816(s[i][n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
+                mma16816(sa[j % NA][i][n], a0, a1, a2, a3, qf[n][j][0], qf[n][j][1]);
                 if (kSplit)
-                  mma16816(s[i][n], a0, a1, a2, a3, ql[kSplit ? n : 0][kSplit ? j : 0][0], ql[kSplit ? n : 0][kSplit ? j : 0][1]);
+                  mma16816(sa[j % NA][i][n], a0, a1, a2, a3, ql[kSplit ? n : 0][kSplit ? j : 0][0], ql[kSplit ? n : 0][kSplit ? j : 0][1]);
               }
             }
         }
+        uint32_t vw[NS][4][D / 32];   // values: the thread's four tokens of a slice, D / 8 bytes at column g
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int row = krow + (u + i) * kslice + box + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
+            if (D == 128) {
+              const uint4 x = *reinterpret_cast<const uint4*>(sk + swz<D>(row, g * 16));
+              vw[i][r][0] = x.x; vw[i][r][1] = x.y; vw[i][r][D / 32 - 2] = x.z; vw[i][r][D / 32 - 1] = x.w;
+            } else {
+              const uint2 x = *reinterpret_cast<const uint2*>(sk + swz<D>(row, g * 8));
+              vw[i][r][0] = x.x; vw[i][r][1] = x.y;
+            }
+          }
+#pragma unroll
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              s[i][n][c] = sa[0][i][n][c];
+#pragma unroll
+              for (int x = 1; x < NA; ++x) s[i][n][c] += sa[x][i][n][c];
+            }
         // to log2 units with the value scale, from the row's reference; tokens that a row does not see
         auto hidden = [&](int n, int c) { return kEdge && at + 8 * (c >> 1) + token_of(g) >= lim[n][c & 1]; };
         float p[NS][NT][4];
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          const float ks = si.ks[slot + u + i], lv = si.lv[slot + u + i];
+          const float ks = sc[u + i].x, lv = sc[u + i].y;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -663,7 +700,7 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int i = 0; i < NS; ++i)
 #pragma unroll
                 for (int e = c; e < 4; e += 2) {
-                  p[i][n][e] = hidden(n, e) ? -INFINITY : fmaf(s[i][n][e], si.ks[slot + u + i] * rs[n][c], si.lv[slot + u + i]);
+                  p[i][n][e] = hidden(n, e) ? -INFINITY : fmaf(s[i][n][e], sc[u + i].x * rs[n][c], sc[u + i].y);
                   m = fmaxf(m, p[i][n][e]);
                 }
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
@@ -687,7 +724,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          const float iv = si.iv[slot + u + i];
+          const float iv = sc[u + i].z;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
@@ -713,27 +750,14 @@ __global__ void __launch_bounds__(kThreads, 2)
               pl[kSplit ? n : 0][1] = transpose8x8(pack_f16(x[2] - y1.x, x[3] - y1.y));
             }
           }
-          // values: this thread's four tokens, D / 8 bytes at column g
-          uint32_t vw[4][D / 32];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) {
-            const int row = krow + (u + i) * kslice + box + 8 * (r >> 1) + token_of(2 * t4 + (r & 1));
-            if (D == 128) {
-              const uint4 x = *reinterpret_cast<const uint4*>(sk + swz<D>(row, g * 16));
-              vw[r][0] = x.x; vw[r][1] = x.y; vw[r][D / 32 - 2] = x.z; vw[r][D / 32 - 1] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(sk + swz<D>(row, g * 8));
-              vw[r][0] = x.x; vw[r][1] = x.y;
-            }
-          }
           auto weigh = [&](int sees) {
             bool seen[4];   // of the thread's four tokens
 #pragma unroll
             for (int r = 0; r < 4; ++r) seen[r] = !kEdge || at + 8 * (r >> 1) + token_of(2 * t4 + (r & 1)) < sees;
 #pragma unroll
             for (int c = 0; c < D / 32; ++c) {
-              const uint32_t v0 = seen[0] ? vw[0][c] : 0u, v1 = seen[1] ? vw[1][c] : 0u;
-              const uint32_t v2 = seen[2] ? vw[2][c] : 0u, v3 = seen[3] ? vw[3][c] : 0u;
+              const uint32_t v0 = seen[0] ? vw[i][0][c] : 0u, v1 = seen[1] ? vw[i][1][c] : 0u;
+              const uint32_t v2 = seen[2] ? vw[i][2][c] : 0u, v3 = seen[3] ? vw[i][3][c] : 0u;
               // bytes of the same d from the tokens of a pair, side by side
               const uint32_t lo01 = __byte_perm(v0, v1, 0x5140), hi01 = __byte_perm(v0, v1, 0x7362);
               const uint32_t lo23 = __byte_perm(v2, v3, 0x5140), hi23 = __byte_perm(v2, v3, 0x7362);
@@ -772,20 +796,21 @@ __global__ void __launch_bounds__(kThreads, 2)
       constexpr int kSide = kSlices > 1 && NT * D <= 128 ? 2 : 1;
       bool whole = tok + 16 * kSlices <= len - a.n_q + 1;
 #pragma unroll
-      for (int u = 0; u < kSlices; ++u) whole = whole && si.ks[slot + u] != 0.f;
+      for (int u = 0; u < kSlices; ++u) whole = whole && sc[u].x != 0.f;
       if (whole) {
 #pragma unroll 1
         for (int u = 0; u < kSlices; u += kSide) slices(std::integral_constant<int, kSide>{}, std::false_type{}, u, 0);
       } else {
 #pragma unroll 1
         for (int u = 0; u < kSlices; ++u)
-          if (tok + 16 * u < len && si.ks[slot + u] != 0.f) slices(One{}, std::true_type{}, u, tok + 16 * u);
+          if (tok + 16 * u < len && sc[u].x != 0.f) slices(One{}, std::true_type{}, u, tok + 16 * u);
       }
     }
-    const UnitInfo u{si.seq, si.head, row0, (flags & (kEnds | kFinal)) | (begins ? kBegins : 0)};
+    const UnitInfo u{where.x, where.y, row0, (flags & (kEnds | kFinal)) | (begins ? kBegins : 0)};
     __syncwarp();
     if (lane == 0) mbar_arrive(&empty[st]);
-    if (++st == stages) { st = 0; phase ^= 1; }
+    st = st_next;
+    phase = phase_next;
 
     if (flags & kLast) {   // this stretch of the unit ends: the warp's part to the output's warp
       if (units_done > 0 && !warp_all(mbar_wait(parts_empty, (units_done - 1) & 1, wc, wsite(3, 0, k)))) return;
