@@ -55,7 +55,7 @@ using kvc::kInt8;
 
 constexpr int kWarps = 4;              // consumer warps
 constexpr int kThreads = 32 * (kWarps + 2);   // and the producer's and the output's warp
-constexpr int kEarly = 4;              // tiles that a stretch starts with before their scales have come
+constexpr int kEarly = 2;              // tiles that a stretch starts with before their scales have come
 constexpr int kJoinThreads = 256;
 constexpr int kJoinLanes = 16;        // at most, for a piece of a joined unit
 constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
@@ -357,74 +357,89 @@ __global__ void __launch_bounds__(kThreads, 2)
       any = any || todo;
       const uint32_t blocks = (live >> (lane & ~((1 << lppt) - 1))) & ((1u << (1 << lppt)) - 1u);   // of the lane's tile
       const uint32_t bytes = __popc(blocks) * 2 * box * D + (opens ? min(kRows, a.rows - cur.row0) * D * (int)sizeof(Tin) : 0);
-      // a tile's copies: keys and values of each block in one, and the query rows where a unit starts
-      auto issue = [&](int t, int at) {
-        if (lane_tile == t && in_tile == 0) mbar_expect_tx(&full[at], bytes);
+      // Tiles are issued a few at a time, each by its own lanes: `sel` has a bit for each at its first lane, and they go to
+      // the stages from `base` on.
+      const int owner = lane & ~((1 << lppt) - 1);
+      auto stage_of = [&](uint32_t sel, int base, int first_lane) {
+        const int at = base + __popc(sel & ((1u << first_lane) - 1u));
+        return at >= stages ? at - stages : at;
+      };
+      // the copies: keys and values of each block in one, and the query rows where a unit starts
+      auto issue = [&](uint32_t sel, int base) {
+        const bool mine = (sel >> owner) & 1u;
+        const int at = stage_of(sel, base, owner);
+        if (mine && in_tile == 0) mbar_expect_tx(&full[at], bytes);
         __syncwarp();
-        char* dst = smem + at * S::STAGE;
-        if (lane_tile == t && cur.id >= 0)
-          tma_load_4d(dst + in_tile * 2 * box * D, &tm, &full[at], 0, (int)(((long long)cur.tile * kTile) & (bs - 1)), 0,
+        if (mine && cur.id >= 0)
+          tma_load_4d(smem + at * S::STAGE + in_tile * 2 * box * D, &tm, &full[at], 0, (int)(((long long)cur.tile * kTile) & (bs - 1)), 0,
                       cur.id * a.Hkv + cur.head);
-        const int owner = t << lppt;
-        if ((opening >> owner) & 1u) {   // rows are (token, head) pairs: one copy for each token's heads
-          const int seq = __shfl_sync(0xffffffffu, cur.seq, owner), head = __shfl_sync(0xffffffffu, cur.head, owner);
-          const int r0 = __shfl_sync(0xffffffffu, cur.row0, owner), r1 = min(r0 + kRows, a.rows);
+        for (uint32_t open = sel & opening; open; open &= open - 1u) {   // rows are (token, head) pairs: one copy for each token's heads
+          const int from = __ffs(open) - 1;
+          const int seq = __shfl_sync(0xffffffffu, cur.seq, from), head = __shfl_sync(0xffffffffu, cur.head, from);
+          const int q_at = __shfl_sync(0xffffffffu, at, from);
+          const int r0 = __shfl_sync(0xffffffffu, cur.row0, from), r1 = min(r0 + kRows, a.rows);
           const int i = a.by_G(r0) + lane, lo = max(r0, i * a.G), hi = min(r1, (i + 1) * a.G);
           if (lo < hi)
-            bulk_load(dst + S::KV + (lo - r0) * D * sizeof(Tin),
+            bulk_load(smem + q_at * S::STAGE + S::KV + (lo - r0) * D * sizeof(Tin),
                       static_cast<const Tin*>(a.q) + ((size_t)seq * a.n_q + i) * a.qstride + (size_t)(head * a.G + lo - i * a.G) * D,
-                      (hi - lo) * D * sizeof(Tin), &full[at]);
+                      (hi - lo) * D * sizeof(Tin), &full[q_at]);
         }
       };
       float ks, lv, iv;   // of the lane's block
-      // a tile's description for the consumers; the scales once for each 16 tokens
-      auto publish = [&](int t, int at) {
-        StageInfo& si = info[at];
-        if (lane_tile == t) {
+      // the tiles' descriptions for the consumers; the scales once for each 16 tokens
+      auto publish = [&](uint32_t sel, int base) {
+        const bool mine = (sel >> owner) & 1u;
+        const int at = stage_of(sel, base, owner);
+        if (mine) {
+          StageInfo& si = info[at];
           for (int e = 0; e < box / 16; ++e) si.scale[in_tile * (box / 16) + e] = make_float4(ks, lv, iv, 0.f);
           if (in_tile == 0) {
             *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, cur.head, cur.row0, cur.tile * kTile);
-            *reinterpret_cast<int4*>(&si.len) = make_int4(lens[cur.seq], flags, 0, 0);
+            *reinterpret_cast<int2*>(&si.len) = make_int2(lens[cur.seq], flags);
           }
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&full[at]);
+        if (mine && in_tile == 0) mbar_arrive(&full[at]);
       };
-      auto next_tile = [&]() {
-        const int t = (__ffs(todo) - 1) >> lppt;
-        todo &= todo - 1u;
-        return t;
+      // up to n of the tiles to do
+      auto take = [&](int n) {
+        uint32_t rest = todo;
+        for (int i = 0; i < n; ++i) rest &= rest - 1u;
+        const uint32_t sel = todo & ~rest;
+        todo = rest;
+        return sel;
       };
-      int early[kEarly], n_early = 0;
-      if (pb == p0)   // the first tiles' copies do not wait for their scales
-#pragma unroll
-        for (int i = 0; i < kEarly; ++i)
-          if (todo && i < stages) {
-            early[i] = next_tile();
-            issue(early[i], i);
-            n_early = i + 1;
-          }
+      uint32_t early = 0u;
+      if (pb == p0) {   // the first tiles' copies do not wait for their scales
+        early = take(1);
+        issue(early, 0);
+        const uint32_t more = take(min(stages, kEarly) - 1);
+        issue(more, 1);
+        early |= more;
+      }
       ks = cur.id >= 0 ? cur.ks : 0.f;
       lv = __log2f(cur.vs);      // (both exact for a power of two)
       iv = __frcp_rn(cur.vs);
       if (pb == p0) {
-#pragma unroll
-        for (int i = 0; i < kEarly; ++i)
-          if (i < n_early) publish(early[i], i);
-        issued = n_early;
-        st = n_early == stages ? 0 : n_early;
-        turn = n_early == stages ? 1 : 0;
+        publish(early, 0);
+        issued = __popc(early);
+        st = issued == stages ? 0 : issued;
+        turn = issued == stages ? 1 : 0;
       }
       fetch_scales(next);
       const Item later = locate(pb + 2 * batch, next.seq);
       while (todo) {
+        // wait for one stage; a second tile goes along if its stage is free by now
         if (turn > 0) ok = warp_all(mbar_wait(&empty[st], (turn - 1) & 1, wc, wsite(1, st, turn)));
         if (!ok) break;
-        const int t = next_tile();
-        issue(t, st);
-        publish(t, st);
-        issued = min(issued + 1, stages);
+        const int base = st;
         if (++st == stages) { st = 0; ++turn; }
+        const bool two = (todo & (todo - 1u)) && (turn == 0 || warp_all(mbar_test(&empty[st], (turn - 1) & 1)));
+        if (two && ++st == stages) { st = 0; ++turn; }
+        const uint32_t sel = take(two ? 2 : 1);
+        issue(sel, base);
+        publish(sel, base);
+        issued = min(issued + __popc(sel), stages);
       }
       // the unit that goes on behind this stretch, for the join
       if (real && final && !ends && in_tile == 0) {
