@@ -74,7 +74,6 @@ struct Divisor {
     return x;
   }
   __device__ __forceinline__ int operator()(int n) const { return (int)(((uint64_t)(uint32_t)n * m) >> (31 + s)); }
-  __device__ __forceinline__ long long of_long(long long n) const { return n >> 31 ? n / d : (*this)((int)n); }
 };
 // A unit that several CTAs have parts of, as each of them but the last notes it down for the join.
 struct Split {
@@ -203,10 +202,6 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
 // (its query operands and its output cost that much), cut into equal stretches of `per` places, one for each CTA.  The
 // tiles of one unit lie in consecutive stretches.
 constexpr int kUnitCost = 2;
-// a / b of numbers that are not negative, in 32 bits where they fit (the long division takes several times as long)
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  return (unsigned long long)(a | b) >> 32 ? a / b : (long long)((uint32_t)a / (uint32_t)b);
-}
 
 template <typename Tin, int D, KvType T, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
@@ -289,11 +284,11 @@ __global__ void __launch_bounds__(kThreads, 2)
     const int batch = 32 >> lppt;                    // tiles looked up at once, a lane per block
     const int in_tile = lane & ((1 << lppt) - 1), lane_tile = lane >> lppt;
     // this CTA's stretch of the line
-    const long long W = (long long)line[a.B] * units, per = a.by_ctas.of_long(W + gridDim.x - 1);
-    const long long p0 = min(W, per * cta), p1 = min(W, per * (cta + 1));
+    const int W = line[a.B] * units, per = a.by_ctas(W + (int)gridDim.x - 1);   // (the whole line fits 31 bits)
+    const int p0 = min(W, per * cta), p1 = min(W, p0 + per);
     // the last sequence whose places begin at or before p0, 32 probes at a time
     int seq0 = 0;
-    for (int n = a.B, f = (int)a.by_units.of_long(p0); n > 1;) {
+    for (int n = a.B, f = a.by_units(p0); n > 1;) {
       const int step = (n + 31) >> 5;
       const uint32_t below = __ballot_sync(0xffffffffu, lane * step < n && line[min(seq0 + lane * step, a.B)] <= f);
       const int hit = 31 - __clz(below);   // (the first probe always is)
@@ -303,30 +298,30 @@ __global__ void __launch_bounds__(kThreads, 2)
     struct Item { int seq, head, row0, tile, tiles, id; float ks, vs; };   // tile < tiles where there is one
     // The lane's block of the batch of places that starts at p: where it belongs, then its number (`id`, as the table
     // has it), then its scales.  Each step's load is used a batch later, so none is waited for but the first.
-    auto locate = [&](long long p, int lo) {
+    auto locate = [&](int p, int lo) {
       Item it{lo, 0, 0, 0, 0, -1, 0.f, 1.f};
       p += lane_tile;
       if (p < p1) {
-        for (int near = 0; near < 4 && (long long)line[lo + 1] * units <= p; ++near) ++lo;
-        if ((long long)line[lo + 1] * units <= p) {
+        for (int near = 0; near < 4 && line[lo + 1] * units <= p; ++near) ++lo;
+        if (line[lo + 1] * units <= p) {
           int hi = a.B;   // line[lo] * units <= p < line[hi] * units
           while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if ((long long)line[mid] * units <= p) lo = mid;
+            if (line[mid] * units <= p) lo = mid;
             else hi = mid;
           }
         }
-        const long long r = p - (long long)line[lo] * units;
+        const uint32_t r = p - line[lo] * units;
         it.seq = lo;
         it.tiles = first[lo + 1] - first[lo];
-        const int unit = (int)quotient(r, it.tiles + kUnitCost);
-        it.tile = (int)(r - (long long)unit * (it.tiles + kUnitCost));
+        const int unit = (int)(r / (uint32_t)(it.tiles + kUnitCost));
+        it.tile = (int)r - unit * (it.tiles + kUnitCost);
         it.head = unit;
         if (a.row_tiles > 1) {
           it.head = a.by_row_tiles(unit);
           it.row0 = (unit - it.head * a.row_tiles) * kMaxRows;
         }
-        const long long tok = (long long)it.tile * kTile + in_tile * box;
+        const int tok = it.tile * kTile + in_tile * box;   // (a row's tokens fit 31 bits, with a tile to spare)
         if (it.tile < it.tiles && tok < lens[lo]) it.id = a.table[(size_t)lo * a.width + (tok >> a.lbs)];
       }
       return it;
@@ -345,8 +340,8 @@ __global__ void __launch_bounds__(kThreads, 2)
     bool ok = true, any = false;
     if (lane == 0) a.split[cta].seq = -1;   // (written again by the lane that finds a unit that goes on)
     __syncwarp();
-    for (long long pb = p0; pb < p1 && ok; pb += batch) {
-      const long long p = pb + lane_tile;
+    for (int pb = p0; pb < p1 && ok; pb += batch) {
+      const int p = pb + lane_tile;
       const bool real = cur.tile < cur.tiles;
       const bool opens = cur.tile == 0 || p == p0, ends = cur.tile == cur.tiles - 1;
       const bool final = p + 1 + (ends ? kUnitCost : 0) >= p1;
@@ -371,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2)
         if (mine && in_tile == 0) mbar_expect_tx(&full[at], bytes);
         __syncwarp();
         if (mine && cur.id >= 0)
-          tma_load_4d(smem + at * S::STAGE + in_tile * 2 * box * D, &tm, &full[at], 0, (int)(((long long)cur.tile * kTile) & (bs - 1)), 0,
+          tma_load_4d(smem + at * S::STAGE + in_tile * 2 * box * D, &tm, &full[at], 0, (cur.tile * kTile) & (bs - 1), 0,
                       cur.id * a.Hkv + cur.head);
         for (uint32_t open = sel & opening; open; open &= open - 1u) {   // rows are (token, head) pairs: one copy for each token's heads
           const int from = __ffs(open) - 1;
@@ -419,7 +414,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       ks = cur.id >= 0 ? cur.ks : 0.f;
       lv = __log2f(cur.vs);      // (both exact for a power of two)
-      iv = __frcp_rn(cur.vs);
+      iv = __fdividef(1.f, cur.vs);
       if (pb == p0) {
         publish(early, 0);
         issued = __popc(early);
@@ -443,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
       // the unit that goes on behind this stretch, for the join
       if (real && final && !ends && in_tile == 0) {
-        const int c0 = (int)quotient(p - cur.tile, per), parts = (int)quotient(p - cur.tile + cur.tiles - 1, per) - c0 + 1;
+        const int c0 = (p - cur.tile) / per, parts = (p - cur.tile + cur.tiles - 1) / per - c0 + 1;
         const int n_rows = min(kRows, a.rows - cur.row0), share = (n_rows * (D / 4) + parts - 2) / (parts - 1);
         int log_lanes = 0;
         while ((2 << log_lanes) <= min(kJoinLanes, parts) && (share << (log_lanes + 1)) <= kJoinThreads) ++log_lanes;

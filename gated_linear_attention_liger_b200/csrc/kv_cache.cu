@@ -293,10 +293,11 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   const int per16 = dt == LIGER_BF16 ? 8 : 4;
   if (q_stride < (long long)Hq * d || q_stride % per16)
     return fail(LIGER_ERR_INVALID_ARG, "the query's token stride must be at least Hq * d elements and a multiple of 16 bytes");
-  const int tile = liger::ca::tile_tokens(d);
-  const long long tiles = (long long)B * (((long long)table_width * block_size + tile - 1) / tile);
-  if ((long long)n_blocks * Hkv > 0x7fffffffLL || tiles > 0x7fffffffLL - 65536)
-    return fail(LIGER_ERR_UNSUPPORTED, "cache too large");
+  const int tile = liger::ca::tile_tokens(d), row_tiles = (int)((rows + liger::ca::kMaxRows - 1) / liger::ca::kMaxRows);
+  // the kernel's line of work, were all sequences as long as their rows of the table
+  const long long places = (((long long)table_width * block_size + tile - 1) / tile + liger::ca::kUnitCost) * B;
+  if ((long long)n_blocks * Hkv > 0x7fffffffLL || places > (0x7fffffffLL - (1 << 20)) / ((long long)Hkv * row_tiles))
+    return fail(LIGER_ERR_UNSUPPORTED, "too large: n_blocks * Hkv and B * table_width * block_size / %d * Hkv must fit 31 bits", tile);
   if (!q || !cache || !scales || !block_table || !seq_lens || !out)
     return fail(LIGER_ERR_INVALID_ARG, "all pointers must be non-null");
   const void* ptrs[] = {q, cache, out, workspace};
@@ -347,7 +348,7 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   a.n_blocks = n_blocks;
   a.lbs = log2_block(block_size);
   a.rows = (int)rows;
-  a.row_tiles = (int)((rows + liger::ca::kMaxRows - 1) / liger::ca::kMaxRows);
+  a.row_tiles = row_tiles;
   a.by_units = liger::ca::Divisor::of(Hkv * a.row_tiles);
   a.by_row_tiles = liger::ca::Divisor::of(a.row_tiles);
   a.by_G = liger::ca::Divisor::of(a.G);

@@ -79,6 +79,7 @@ def test_append_of_nothing_is_ok(lib):
     (dict(ws=None), INVALID), (dict(wsb=1024), INVALID), (dict(scales=4), INVALID), (dict(lens=2), INVALID),
     (dict(nq=17), UNSUPPORTED), (dict(d=32), UNSUPPORTED), (dict(bs=512), UNSUPPORTED), (dict(B=9000), UNSUPPORTED),
     (dict(Hkv=256, Hq=256, qs=256 * 64, n=1 << 24, bs=16), UNSUPPORTED),
+    (dict(B=8192, width=1 << 20, bs=128), UNSUPPORTED),
 ])
 def test_attention_rejects(lib, kw, status):
     assert _attend(lib, **kw) == status
