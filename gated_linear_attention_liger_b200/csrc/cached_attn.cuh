@@ -198,17 +198,18 @@ __device__ __forceinline__ void mbar_expect_tx(uint64_t* bar, uint32_t bytes) {
   asm volatile("mbarrier.expect_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(bytes) : "memory");
 }
 
-// The line of work: sequence by sequence, unit by unit, a place for each tile and kUnitCost more behind a unit's last one
-// (its query operands and its output cost that much), cut into equal stretches of `per` places, one for each CTA.  The
-// tiles of one unit lie in consecutive stretches.
-constexpr int kUnitCost = 2;
+// The line of work: sequence by sequence, unit by unit, a place for each tile and unit_cost more behind a unit's last one
+// (its query operands and its output cost that much; with 16 rows a place more or less took 5 to 10% longer on short
+// units, with 8 rows 1%), cut into equal stretches of `per` places, one for each CTA.  The tiles of one unit lie in
+// consecutive stretches.
+constexpr int unit_cost(int nt) { return nt + 1; }   // nt: query rows in eights, at most 2
 
 template <typename Tin, int D, KvType T, int NT>
 __global__ void __launch_bounds__(kThreads, 2)
     cached_attn_kernel(const __grid_constant__ CUtensorMap tm, Args a, int stages) {
   using S = Smem<Tin, D, NT>;
   constexpr bool kSplit = sizeof(Tin) == 4;                 // fp32: two fp16 terms of q and of p
-  constexpr int kRows = 8 * NT, kTile = tile_tokens(D);
+  constexpr int kRows = 8 * NT, kTile = tile_tokens(D), kUnitCost = unit_cost(NT);
   extern __shared__ __align__(1024) char smem_raw[];
   char* smem = reinterpret_cast<char*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   StageInfo* info = reinterpret_cast<StageInfo*>(smem + stages * S::STAGE);

@@ -228,11 +228,13 @@ liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_l
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (n_slots <= kOneCtaSlots) {
+    liger::mark_dominant_start(s);
     e = launch_assign<true, true>(a, 1, s);
   } else {
     const long long ctas = ((long long)n_slots + 4 * liger::kvc::kAssignThreads - 1) / (4 * liger::kvc::kAssignThreads);
     const long long most = 2LL * liger::device_sm_count();   // (they are all resident: each scans all sequences)
     const int n = (int)(ctas < most ? ctas : most);
+    liger::mark_dominant_start(s);
     if (seq_lens_out != seq_lens && free_span_out != free_span) {
       e = launch_assign<true, true>(a, n, s);
     } else {   // every CTA reads the lengths and the span: they change when all have
@@ -240,6 +242,7 @@ liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_l
       if (e == cudaSuccess) e = launch_assign<false, true>(a, 1, s);
     }
   }
+  liger::mark_dominant_stop(s);
   return e == cudaSuccess ? LIGER_OK : cuda_fail(e, "cache assignment launch");
 }
 
@@ -267,8 +270,10 @@ liger_status liger_kv_cache_append(const void* k, const void* v, const int32_t* 
   const liger::kvc::AppendArgs a{k, v, slot_map, static_cast<uint8_t*>(cache), scales, (long)k_stride, (long)v_stride,
                                  n_tokens, Hkv, n_blocks * block_size};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  liger::mark_dominant_start(s);
   const cudaError_t e = dt == LIGER_BF16 ? append_t<__nv_bfloat16>(a, d, block_size, kv_dt, s)
                                          : append_t<float>(a, d, block_size, kv_dt, s);
+  liger::mark_dominant_stop(s);
   return e == cudaSuccess ? LIGER_OK : cuda_fail(e, "cache append launch");
 }
 
@@ -288,14 +293,14 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   if (st != LIGER_OK) return st;
   if (n_q < 1) return fail(LIGER_ERR_INVALID_ARG, "need n_q >= 1 (n_q=%d)", n_q);
   const long long rows = (long long)n_q * (Hq / Hkv);
-  if (n_q > LIGER_CACHED_MAX_NEW || rows > 65536 || Hkv > 65536)
+  if (n_q > LIGER_CACHED_MAX_NEW || rows > 65536 || Hkv > 65536 || (long long)n_q * Hq > 1 << 20)
     return fail(LIGER_ERR_UNSUPPORTED, "n_q=%d new tokens a sequence (at most %d), Hq=%d", n_q, LIGER_CACHED_MAX_NEW, Hq);
   const int per16 = dt == LIGER_BF16 ? 8 : 4;
   if (q_stride < (long long)Hq * d || q_stride % per16)
     return fail(LIGER_ERR_INVALID_ARG, "the query's token stride must be at least Hq * d elements and a multiple of 16 bytes");
   const int tile = liger::ca::tile_tokens(d), row_tiles = (int)((rows + liger::ca::kMaxRows - 1) / liger::ca::kMaxRows);
   // the kernel's line of work, were all sequences as long as their rows of the table
-  const long long places = (((long long)table_width * block_size + tile - 1) / tile + liger::ca::kUnitCost) * B;
+  const long long places = (((long long)table_width * block_size + tile - 1) / tile + liger::ca::unit_cost(2)) * B;
   if ((long long)n_blocks * Hkv > 0x7fffffffLL || places > (0x7fffffffLL - (1 << 20)) / ((long long)Hkv * row_tiles))
     return fail(LIGER_ERR_UNSUPPORTED, "too large: n_blocks * Hkv and B * table_width * block_size / %d * Hkv must fit 31 bits", tile);
   if (!q || !cache || !scales || !block_table || !seq_lens || !out)
