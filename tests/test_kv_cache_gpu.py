@@ -321,6 +321,27 @@ def test_attention_most_sequences(cuda_device):
     _run_attention(rng, cuda_device, lens, 1, 1, 1, 128, 16, INT8, BF16)
 
 
+def test_attention_most_sequences_of_many_rows(cuda_device):
+    """The prefix sums of 8192 sequences beside the largest stages and parts: one CTA an SM."""
+    rng = np.random.default_rng(25)
+    lens = [int(x) for x in rng.integers(0, 6, 8192)]
+    lens[77], lens[8191] = 300, 1000
+    _run_attention(rng, cuda_device, lens, 4, 4, 1, 128, 16, E4M3, FP32)
+
+
+@pytest.mark.parametrize("seed", range(24))
+def test_attention_drawn_cases(seed, cuda_device):
+    """Sizes drawn over the whole range: units of one tile to many, split and whole, stretches that
+    end in a unit, between units and behind the last one."""
+    rng = np.random.default_rng(1000 + seed)
+    B = int(np.exp(rng.uniform(0, np.log(60))))
+    top = int(np.exp(rng.uniform(0, np.log(60000 // B))))
+    lens = [int(x) for x in rng.integers(0, top + 1, B)]
+    d, G = int(rng.choice([64, 128])), int(rng.choice([1, 2, 3, 4, 5, 8, 17]))
+    _run_attention(rng, cuda_device, lens, int(rng.choice([1, 1, 2, 4, 7, 16])), G, int(rng.choice([1, 2, 3])), d,
+                   int(rng.choice([16, 32, 64, 128])), E4M3 if rng.random() < 0.5 else INT8, BF16 if rng.random() < 0.6 else FP32)
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 def test_attention_peaked_scores_and_unlike_scales(dtype, cuda_device):
     """Scores far apart (the reference is raised again and again, late in the sequence too), and
@@ -580,3 +601,23 @@ def test_launches_are_counted(cuda_device):
     before = ops.kernel_launches()
     ops.cached_attention(q, cache, scales, i32(table, cuda_device), i32([20], cuda_device))
     assert ops.kernel_launches() == before + 2
+
+
+def test_timing_events_bracket_the_kernels(cuda_device):
+    """liger_set_timing_events brackets each operator's kernel, as it does the other entry points'."""
+    dev = cuda_device
+    c = ops.kv_cache_new(8, 2, 64, 16, 3, 32, device=dev)
+    k = torch.ones(3, 2, 64, dtype=BF16, device=dev)
+    a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    a.record(); b.record()
+    new = i32([1, 1, 1], dev)
+    calls = [lambda: ops.kv_cache_assign(new, c["seq_lens"], c["block_table"], c["free_blocks"], c["free_span"], 16, 3,
+                                         seq_lens_out=c["seq_lens"], free_span_out=c["free_span"]),
+             lambda: ops.kv_cache_append(k, k, i32([0, 16, 32], dev), c["cache"], c["scales"]),
+             lambda: ops.cached_attention(k, c["cache"], c["scales"], c["block_table"], c["seq_lens"])]
+    for call in calls:
+        ops.set_timing_events(a, b)
+        call()
+        ops.set_timing_events(None, None)
+        torch.cuda.synchronize()
+        assert 0 < a.elapsed_time(b) < 1000
