@@ -175,7 +175,7 @@ liger_status launch_attn(const CUtensorMap& tm, liger::ca::Args a, int ctas, cud
   int stages = (kShare - fixed) / (int)S::STAGE;
   if (stages < 3) {   // thousands of sequences: their prefix sums take the second CTA's place
     stages = (kAlone - fixed) / (int)S::STAGE;
-    ctas /= kCtasPerSm;
+    ctas = (ctas + kCtasPerSm - 1) / kCtasPerSm;
   }
   if (stages > S::MAX_STAGES) stages = S::MAX_STAGES;
   a.by_ctas = liger::ca::Divisor::of(ctas);
@@ -357,8 +357,11 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   a.by_units = liger::ca::Divisor::of(Hkv * a.row_tiles);
   a.by_row_tiles = liger::ca::Divisor::of(a.row_tiles);
   a.by_G = liger::ca::Divisor::of(a.G);
+  // no more CTAs than the line can have places (short tables)
+  const long long most = places * Hkv * row_tiles;
+  const int ctas = most < L.ctas ? (int)most : L.ctas;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  return dt == LIGER_BF16 ? attn_t<__nv_bfloat16>(tm, a, d, kv_dt, L.ctas, s) : attn_t<float>(tm, a, d, kv_dt, L.ctas, s);
+  return dt == LIGER_BF16 ? attn_t<__nv_bfloat16>(tm, a, d, kv_dt, ctas, s) : attn_t<float>(tm, a, d, kv_dt, ctas, s);
 }
 
 liger_status liger_attn_cached_status(void) {
