@@ -253,17 +253,39 @@ __global__ void __launch_bounds__(kThreads, 2)
     prefetch_tensormap(&tm);
   }
   kvc::pdl_launch_next();
+  __syncthreads();
   kvc::pdl_wait_previous();
 
   const int cap = a.width << a.lbs;
-  // tiles before each sequence: a block scan, each thread over consecutive sequences
-  {
+  auto length = [&](int s) { return min(max(a.lens[s], 0), cap); };
+  auto tiles_of = [&](int len) { return (int)(((long long)len + kTile - 1) / kTile); };
+  // tiles before each sequence, for the producer: its own scan if a warp holds them, else a block's, each thread over
+  // consecutive sequences
+  if (a.B <= 32) {
+    if (warp == kWarps) {
+      const int len = lane < a.B ? length(lane) : 0, n = tiles_of(len);
+      int x = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= o) x += u;
+      }
+      const int seqs = __popc(__ballot_sync(0xffffffffu, n > 0) & ((2u << lane) - 1u));
+      if (lane < a.B) {
+        lens[lane] = len;
+        first[lane + 1] = x;
+        line[lane + 1] = x + kUnitCost * seqs;
+      }
+      if (lane == 0) first[0] = line[0] = 0;
+      __syncwarp();
+    }
+  } else {
     const int per = (a.B + kThreads - 1) / kThreads;
     const int s0 = tid * per, s1 = min(a.B, s0 + per);
     int sum = 0, some = 0;
     for (int s = s0; s < s1; ++s) {
-      const int len = min(max(a.lens[s], 0), cap), n = (int)(((long long)len + kTile - 1) / kTile);
-      lens[s] = len;
+      lens[s] = length(s);
+      const int n = tiles_of(lens[s]);
       sum += n;
       some += n > 0;
     }
@@ -278,7 +300,7 @@ __global__ void __launch_bounds__(kThreads, 2)
     int run = x - sum, seqs = y - some;
     for (int w = 0; w < warp; ++w) { run += part[w]; seqs += part[8 + w]; }
     for (int s = s0; s < s1; ++s) {
-      const int n = (int)(((long long)lens[s] + kTile - 1) / kTile);
+      const int n = tiles_of(lens[s]);
       first[s] = run;
       line[s] = run + kUnitCost * seqs;
       run += n;
@@ -480,7 +502,7 @@ __global__ void __launch_bounds__(kThreads, 2)
   if (warp == kWarps + 1) {   // ---------------- output
     // sequences without tokens: zero rows
     for (int s = cta; s < a.B; s += gridDim.x)
-      if (first[s + 1] == first[s]) {
+      if (length(s) == 0) {
         uint4* o = reinterpret_cast<uint4*>(static_cast<Tin*>(a.out) + (size_t)s * a.n_q * a.Hq * D);
         const int n16 = a.n_q * a.Hq * D * (int)sizeof(Tin) / 16;
         for (int i = lane; i < n16; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
