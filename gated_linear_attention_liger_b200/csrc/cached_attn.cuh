@@ -41,11 +41,12 @@
 // Roundings to fewer bits: p to fp16 (2^-11 of itself; fp32 outputs: two terms, 2^-22), the output to its type.
 //
 // Measured on a B200 (calls back to back in a CUDA graph; bytes of the cache, queries and outputs over the 6570 GB/s of a
-// copy): 64 sequences of 2048 to 8192 tokens, Hq 32, Hkv 8, d 128, e4m3: 115.6 us, 0.89 of it (without the products
-// 114.9: the stream bounds it); one of 131072 tokens: 50.5 us, 0.81; 256 of up to 1500 tokens in blocks of 16, int8: 82.8 us,
-// 0.73; 4 new tokens each for 32 sequences of up to 6000, d 64: 34.6 us, 0.44 (16 rows a unit: the consumers' latencies
-// bound it, two warps a scheduler at 168 registers); one of 1000 tokens: 9.7 us, of which 3 go by before the first tile has
-// come, 1 in it, 2 in its output and 3.5 in the join.
+// copy): 64 sequences of 2048 to 8192 tokens, Hq 32, Hkv 8, d 128, e4m3: 114.8 us, 0.89 of it (the copies without the
+// products took as long: the stream bounds it); one of 131072 tokens: 49.4 us, 0.83; 256 of up to 1500 tokens in blocks of 16,
+// int8: 82.2 us, 0.74; 4 new tokens each for 32 sequences of up to 6000, d 64: 33.8 us, 0.45 (16 rows a unit: the consumers'
+// latencies bound it, two warps a scheduler at 168 registers; 32 rows a unit spilled and took 117 us where two units of 16
+// take 71); one of 1000 tokens: 8.0 us, of latencies (the first tile comes after 2.5, its products take 1, its output 1.5,
+// the join 3).
 #pragma once
 
 #include <cuda_bf16.h>
