@@ -415,6 +415,9 @@ liger_status liger_kv_cache_append(const void* k, const void* v, const int32_t* 
  *   workspace  liger_attn_cached_workspace_size(d) bytes of device scratch (16-byte
  *        aligned; contents on entry ignored, nothing kept in it between calls, so calls
  *        in stream order may share it).
+ * Sizes beyond these are LIGER_ERR_UNSUPPORTED: n_q * (Hq / Hkv) <= 65536, n_q * Hq <= 2^20, n_blocks * Hkv in 31 bits, and
+ * in 31 bits the tiles of 64 (d = 128) or 128 (d = 64) tokens that B full rows of the table hold, times Hkv, times the
+ * query rows of a kv head in sixteens.
  * Results do not depend on timing.  n_q is at most LIGER_CACHED_MAX_NEW.  Every internal
  * wait is bounded; liger_attn_cached_status() reports whether any call on the current
  * device gave up since the last query (synchronous read; call it after the stream has
