@@ -79,6 +79,17 @@ liger_status cuda_check(const char* where) {
   return LIGER_OK;
 }
 
+// Makes the device's context current in the calling host thread, once a thread: the tensor maps' encoder is the driver's
+// and fails where none is, as in a thread whose first CUDA call comes through here.  A runtime call that asks about a
+// kernel does it (and is legal in a stream capture).
+void bind_context() {
+  thread_local bool bound = false;
+  if (bound) return;
+  cudaFuncAttributes attr;
+  bound = cudaFuncGetAttributes(&attr, liger::advance_pos_kernel) == cudaSuccess;
+  if (!bound) cudaGetLastError();   // (the encoding fails and is reported)
+}
+
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // A named NVTX range over one entry point, for profilers that attach to NVTX
@@ -317,7 +328,10 @@ void mark_dominant_start(cudaStream_t s) { mark_start(s); }
 void mark_dominant_stop(cudaStream_t s) { mark_stop(s); }
 int device_sm_count() { return tc::num_sms(); }
 uint64_t bounded_wait_ns() { return tc::wait_limit_ns(); }
-TensorMapEncodeFn tensor_map_encoder() { return tc::encode_fn(); }
+TensorMapEncodeFn tensor_map_encoder() {
+  bind_context();
+  return tc::encode_fn();
+}
 
 // Whether a prefill with these arguments runs on the tensor-core path, the only one that
 // uses the workspace.
@@ -413,6 +427,7 @@ liger_status liger_attn_prefill(const void* q, const void* k, const void* v, voi
                                  n_seqs, alpha};
     const liger::tc::LaunchHooks hooks{mark_start, mark_stop, count_launches};
     const uint32_t* s0_flags = nullptr;
+    bind_context();
     st = liger::tc::run_prefill(pb, workspace, s, hooks, &s0_flags);
     if (st != LIGER_OK) return fail(st, "%s", liger::tc::last_message());
     if (initial_state) {
@@ -621,6 +636,7 @@ liger_status liger_attn_prefill_backward(const void* q, const void* k, const voi
   liger::bwd::BwdProblem pb{q, k, v, d_out, d_final_state, initial_state, dq, dk, dv, d_initial_state, cu_seqlens,
                             B, Hq, Hkv, (long)T, d, n_seqs, alpha};
   const liger::tc::LaunchHooks hooks{mark_start, mark_stop, count_launches};
+  bind_context();
   st = liger::bwd::run_backward(pb, workspace, s, hooks);
   if (st != LIGER_OK) return fail(st, "%s", liger::tc::last_message());
   return LIGER_OK;
@@ -661,7 +677,7 @@ liger_status liger_attn_full_causal(const void* q, const void* k, const void* v,
   if (n_qblk > 0x7fffffffL || (long)n_seqs > 65535 || Hq > 65535)
     return fail(LIGER_ERR_UNSUPPORTED, "grid too large");
   CUtensorMap mq, mk, mv;
-  const auto enc = reinterpret_cast<liger::fa::EncodeTiledFn>(liger::tc::encode_fn());
+  const auto enc = reinterpret_cast<liger::fa::EncodeTiledFn>(liger::tensor_map_encoder());
   if (!liger::fa::make_map(enc, &mq, q, d, Hq, NT) || !liger::fa::make_map(enc, &mk, k, d, Hkv, NT) ||
       !liger::fa::make_map(enc, &mv, v, d, Hkv, NT))
     return fail(LIGER_ERR_CUDA, "cuTensorMapEncodeTiled failed for the causal attention");
