@@ -112,7 +112,10 @@ cudaError_t launch_assign(const liger::kvc::AssignArgs& a, int ctas, cudaStream_
   auto kern = liger::kvc::assign_kernel<SLOTS, STATE>;
   const size_t smem = liger::kvc::assign_smem_bytes(a.B);
   if (smem > 40 * 1024) {   // (static shared memory counts toward the default 48 KB)
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // the limit belongs to the kernel, not to the call: the most that any call takes, since another thread's call may
+    // set it between this one's setting and launch
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)liger::kvc::assign_smem_bytes(liger::kvc::kMaxSeqs));
     if (e != cudaSuccess) return e;
   }
   return launch(kern, dim3((unsigned)ctas), liger::kvc::kAssignThreads, smem, s, a);
@@ -181,7 +184,8 @@ liger_status launch_attn(const CUtensorMap& tm, liger::ca::Args a, int ctas, cud
   a.by_ctas = liger::ca::Divisor::of(ctas);
   const int smem = (int)S::bytes(stages, a.rows, a.B);
   auto kern = liger::ca::cached_attn_kernel<Tin, D, T, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  // (whatever this call takes: the limit is the kernel's, and calls from other threads set it too)
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlone);
   if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(cached attention)");
   liger::mark_dominant_start(s);
   e = launch(kern, dim3((unsigned)ctas), liger::ca::kThreads, (size_t)smem, s, tm, a, stages);
