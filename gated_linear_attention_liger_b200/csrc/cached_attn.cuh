@@ -34,10 +34,13 @@
 // bytes of a word are one k-step's elements of a thread; for the values, bytes of the same d
 // from two tokens are paired by a byte permute.
 //
-// Softmax: x = s + log2(vs) in log2 units.  p = 2^(x - m) weighs the value codes directly, and
-// the row sum takes p / vs: one running reference m serves both, whatever the scales.  m is
-// raised only when some x exceeds it by 2^15 (a warp vote per tile; the accumulators are then
-// rescaled); p stays below 2^15, inside fp16, and keeps full fp16 precision 2^29 below that.
+// Softmax: with the score s in log2 units, the row sum takes t = 2^(s - m) and the value codes p = t vs, one running
+// reference m for both.  m is raised only when some s + log2(vs) exceeds it by 15 (a warp vote per tile; the accumulators
+// are then rescaled); p stays below 2^15, inside fp16, and keeps full fp16 precision 2^29 below that.  t needs fp32's
+// range: a token's s is up to 64 above s + log2(vs) (append writes no scale below 2^-64; below that one the reference
+// takes log2(vs) as -64), so t is at most 2^79 and a sum of 2^31 of them finite, and in a sequence whose largest value scale is
+// 2^e a weight counts down to 2^(e - 133) of the largest (2^-33 at 2^100).  Rescaling and joining take a sum's factor in two
+// halves, since the references of a zero block (scale 2^-64) and its neighbour may lie more than 2^126 apart.
 // Roundings to fewer bits: p to fp16 (2^-11 of itself; fp32 outputs: two terms, 2^-22), the output to its type.
 //
 // Measured on a B200 (calls back to back in a CUDA graph; bytes of the cache, queries and outputs over the 6570 GB/s of a
@@ -118,7 +121,7 @@ struct StageInfo {
   int seq, head, row0, tok0;           // kv head, first query row, first cached token
   int len, flags;                      // tokens of the sequence; kFirst | kLast | kBegins | kEnds
   int pad0, pad1;
-  float4 scale[8];                     // per 16 tokens: key scale (0: no such block), log2 and reciprocal of the value scale
+  float4 scale[8];                     // per 16 tokens: key scale (0: no such block), log2 of the value scale (at least -64), value scale
 };
 // the first, last tile of this CTA's stretch of the unit / of the unit itself; the stretch's last tile; no tile at all
 enum { kFirst = 1, kLast = 2, kBegins = 4, kEnds = 8, kFinal = 16, kNone = 32 };
@@ -426,14 +429,14 @@ __global__ void __launch_bounds__(kThreads, 2)
                       (hi - lo) * D * sizeof(Tin), &full[q_at]);
         }
       };
-      float ks, lv, iv;   // of the lane's block
+      float ks, lv, vs;   // of the lane's block
       // the tiles' descriptions for the consumers; the scales once for each 16 tokens
       auto publish = [&](uint32_t sel, int base) {
         const bool mine = (sel >> owner) & 1u;
         const int at = stage_of(sel, base, owner);
         if (mine) {
           StageInfo& si = info[at];
-          for (int e = 0; e < box / 16; ++e) si.scale[in_tile * (box / 16) + e] = make_float4(ks, lv, iv, 0.f);
+          for (int e = 0; e < box / 16; ++e) si.scale[in_tile * (box / 16) + e] = make_float4(ks, lv, vs, 0.f);
           if (in_tile == 0) {
             *reinterpret_cast<int4*>(&si.seq) = make_int4(cur.seq, cur.head, cur.row0, cur.tile * kTile);
             *reinterpret_cast<int2*>(&si.len) = make_int2(lens[cur.seq], flags);
@@ -459,8 +462,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         early |= more;
       }
       ks = cur.id >= 0 ? cur.ks : 0.f;
-      lv = __log2f(cur.vs);      // (both exact for a power of two)
-      iv = __fdividef(1.f, cur.vs);
+      vs = cur.vs;
+      lv = fmaxf(__log2f(vs), (float)kvc::kMinScaleExp);   // (decides when the reference is raised, no weight)
       if (pb == p0) {
         publish(early, 0);
         issued = __popc(early);
@@ -531,8 +534,8 @@ __global__ void __launch_bounds__(kThreads, 2)
         const float2 ml = *reinterpret_cast<const float2*>(red_ml + (w * part_rows + r) * 2);
         float m = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-        const float f = ex2(ml.x - m);
-        float l = f * ml.y;
+        const float half = ex2(0.5f * (ml.x - m)), f = half * half;
+        float l = (half * ml.y) * half;
         l += __shfl_xor_sync(0xffffffffu, l, 1);
         l += __shfl_xor_sync(0xffffffffu, l, 2);
         if (at + lane < 4 * n_rows) {
@@ -730,20 +733,22 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
               for (int x = 1; x < NA; ++x) s[i][n][c] += sa[x][i][n][c];
             }
-        // to log2 units with the value scale, from the row's reference; tokens that a row does not see
+        // to log2 units, from the row's reference; tokens that a row does not see
         auto hidden = [&](int n, int c) { return kEdge && at + 8 * (c >> 1) + token_of(g) >= lim[n][c & 1]; };
         float p[NS][NT][4];
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          const float ks = sc[u + i].x, lv = sc[u + i].y;
+          const float ks = sc[u + i].x;
+          float most = -INFINITY;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-              p[i][n][c] = hidden(n, c) ? -INFINITY : fmaf(s[i][n][c], ks * rs[n][c & 1], lv - ref[n][c & 1]);
-              top = fmaxf(top, p[i][n][c]);
+              p[i][n][c] = hidden(n, c) ? -INFINITY : fmaf(s[i][n][c], ks * rs[n][c & 1], -ref[n][c & 1]);
+              most = fmaxf(most, p[i][n][c]);
             }
+          top = fmaxf(top, most + sc[u + i].y);
         }
         if (__any_sync(0xffffffffu, top > kRaiseAt)) {
 #pragma unroll
@@ -756,20 +761,24 @@ __global__ void __launch_bounds__(kThreads, 2)
               for (int i = 0; i < NS; ++i)
 #pragma unroll
                 for (int e = c; e < 4; e += 2) {
-                  p[i][n][e] = hidden(n, e) ? -INFINITY : fmaf(s[i][n][e], sc[u + i].x * rs[n][c], sc[u + i].y);
-                  m = fmaxf(m, p[i][n][e]);
+                  p[i][n][e] = hidden(n, e) ? -INFINITY : s[i][n][e] * (sc[u + i].x * rs[n][c]);
+                  m = fmaxf(m, p[i][n][e] + sc[u + i].y);
                 }
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
               m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
               const float to = fmaxf(ref[n][c], m - kRefBelow);
-              f[c] = ex2(ref[n][c] - to);
+              const float half = ex2(0.5f * (ref[n][c] - to));
+              f[c] = half * half;
               ref[n][c] = to;
-              sum[n][c] *= f[c];
+              sum[n][c] = (sum[n][c] * half) * half;
 #pragma unroll
               for (int i = 0; i < NS; ++i)
 #pragma unroll
-                for (int e = c; e < 4; e += 2) p[i][n][e] -= to;
+                for (int e = c; e < 4; e += 2) {   // (no NaN is dropped; scores so large that `to` rounds away log2(vs) stay in fp16's range)
+                  const float x = p[i][n][e] - to, limit = kRaiseAt - sc[u + i].y;
+                  p[i][n][e] = x > limit ? limit : x;
+                }
             }
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
@@ -780,13 +789,15 @@ __global__ void __launch_bounds__(kThreads, 2)
         }
 #pragma unroll
         for (int i = 0; i < NS; ++i) {
-          const float iv = sc[u + i].z;
+          const float vs = sc[u + i].z;
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int c = 0; c < 4; ++c) p[i][n][c] = ex2(p[i][n][c]);
-            sum[n][0] = fmaf(p[i][n][0] + p[i][n][2], iv, sum[n][0]);
-            sum[n][1] = fmaf(p[i][n][1] + p[i][n][3], iv, sum[n][1]);
+            sum[n][0] += p[i][n][0] + p[i][n][2];
+            sum[n][1] += p[i][n][1] + p[i][n][3];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) p[i][n][c] *= vs;
           }
         }
         // O^T += V^T P^T.  At the end there is one pass for each new token, over the value codes that it sees, and only its
@@ -916,9 +927,9 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(Args a) {
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     float m = kNoRef, l = 0.f;
     auto add = [&](float om, float ol, float4 y) {
-      const float top = fmaxf(m, om), f = ex2(m - top), g = ex2(om - top);
+      const float top = fmaxf(m, om), fh = ex2(0.5f * (m - top)), gh = ex2(0.5f * (om - top)), f = fh * fh, g = gh * gh;
       m = top;
-      l = l * f + ol * g;
+      l = (l * fh) * fh + (ol * gh) * gh;
       x.x = x.x * f + y.x * g; x.y = x.y * f + y.y * g;
       x.z = x.z * f + y.z * g; x.w = x.w * f + y.w * g;
     };

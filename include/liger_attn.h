@@ -408,6 +408,9 @@ liger_status liger_kv_cache_append(const void* k, const void* v, const int32_t* 
  * A query that sees no token (len too short) gets zeros.  A table entry that is no block
  * number stands for tokens that are not there.  Slots behind a sequence's last token may
  * hold anything.
+ * Value scales of one sequence may differ as far as liger_kv_cache_append writes them (2^-64
+ * for a block of zeros beside huge ones): with 2^e the largest, a token's weight counts down to
+ * 2^(e - 133) of the largest weight (2^-33 at 2^100).
  *   q    [B, n_q, Hq, d] dt (in)  tokens q_stride elements apart (at least Hq * d, a
  *        multiple of 16 bytes), heads and elements contiguous
  *   out  [B, n_q, Hq, d] dt (out)

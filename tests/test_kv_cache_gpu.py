@@ -621,3 +621,42 @@ def test_timing_events_bracket_the_kernels(cuda_device):
         ops.set_timing_events(None, None)
         torch.cuda.synchronize()
         assert 0 < a.elapsed_time(b) < 1000
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("order", [[-64, 100], [100, -64], [-64, 0, 100, -30, 60], [100, -64, -64, -64, -64, -64, 20]], ids=str)
+@pytest.mark.parametrize("joined", [False, True], ids=["one_cta", "joined"])
+def test_attention_value_scales_far_apart(joined, order, dtype, cuda_device):
+    """A block of zero values (scale 2^-64) beside one of scale 2^100: its tokens weigh what their scores say, in one
+    slice, over slices and tiles, and where the parts of several CTAs are joined."""
+    rng = np.random.default_rng(28)
+    dev, Hkv, d, bs = cuda_device, 1, 64, 16
+    reps = 64 if joined else 1     # (of each block of the order, side by side)
+    lens = [len(order) * reps * bs - 5]
+    cache, _, table, values, s64 = _attention_case(rng, lens, Hkv, bs, d, INT8, dev, stale=False)
+    s64[..., 0] = 2.0 ** -8
+    for j, e in enumerate(np.repeat(order, reps)):
+        s64[table[0, j], :, 1] = 2.0 ** int(e)
+        if e == -64:
+            values[table[0, j], :, 1] = 0.0
+            cache[int(table[0, j]), :, 1] = 0
+    q = torch.tensor(rng.normal(size=(1, 1, 2, d))).to(dtype)
+    out = ops.cached_attention(q.to(dev), cache, torch.tensor(s64).float().to(dev), i32(table, dev), i32(lens, dev))
+    want = ref.attention(q.double().numpy(), values, s64, table, lens)
+    # a weight's exponent is the score less the row's reference, which holds the value scale: up to 2^8 in size here, so
+    # that its rounding, half a step of at most 2^-16, moves numerator and sum by 2^-17 each
+    got = out.cpu().double().numpy()
+    tol = ref.attention_tolerance(want, dtype, d) + 2 * 2.0 ** -17 * want[1]
+    assert (np.abs(got - want[0]) <= tol).all(), np.nanmax(np.abs(got - want[0]) / tol)
+
+
+def test_append_then_attention_of_zero_and_huge_values(cuda_device):
+    """The same through the append: fp32 values of 2^100 in one block, zeros in the next, equal scores."""
+    dev, d, bs = cuda_device, 64, 16
+    c = ops.kv_cache_new(2, 1, d, bs, 1, 2 * bs, device=dev)
+    v = torch.zeros(2 * bs, 1, d, device=dev)
+    v[:bs] = 2.0 ** 100
+    ops.kv_cache_append(torch.ones(2 * bs, 1, d, device=dev), v, i32(range(2 * bs), dev), c["cache"], c["scales"])
+    out = ops.cached_attention(torch.ones(1, 1, d, device=dev), c["cache"], c["scales"], i32([[0, 1]], dev), i32([2 * bs], dev))
+    # equal scores give equal weights, and 2^100 is a code: the mean, off by the sums' roundings alone
+    assert ((out - 2.0 ** 99).abs() <= 2.0 ** 99 * 2.0 ** -20).all()
