@@ -75,7 +75,7 @@ constexpr int kThreads = 32 * (kWarps + 2);   // and the producer's and the outp
 constexpr int kEarly = 2;              // tiles that a stretch starts with before their scales have come
 constexpr int kJoinThreads = 256;
 constexpr int kJoinLanes = 8;         // at most, for a piece of a joined unit (16: one short sequence 9.6 instead of 8.9 us)
-constexpr float kNoRef = -1e30f;       // reference of a row that has seen nothing
+constexpr float kNoRef = -3e38f;       // reference of a row that has seen nothing: below every finite score
 constexpr float kRefBelow = 7.f;       // the reference is set this far below the maximum,
 constexpr float kRaiseAt = 15.f;       // and raised when a score exceeds it by this much
 

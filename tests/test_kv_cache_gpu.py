@@ -660,3 +660,24 @@ def test_append_then_attention_of_zero_and_huge_values(cuda_device):
     out = ops.cached_attention(torch.ones(1, 1, d, device=dev), c["cache"], c["scales"], i32([[0, 1]], dev), i32([2 * bs], dev))
     # equal scores give equal weights, and 2^100 is a code: the mean, off by the sums' roundings alone
     assert ((out - 2.0 ** 99).abs() <= 2.0 ** 99 * 2.0 ** -20).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n", [1, 5, 5000])
+def test_attention_scores_of_huge_magnitude(n, dtype, cuda_device):
+    """Scores of -2^110 and beyond are scores: a row's output stays the average of the values that they choose, with
+    one token its value."""
+    rng = np.random.default_rng(29)
+    dev, d, bs = cuda_device, 64, 16
+    cache, scales, table, values, s64 = _attention_case(rng, [n], 1, bs, d, INT8, dev)
+    cache[:, :, 0] = -4
+    scales[..., 0] = 2.0 ** 45
+    scales[..., 1] = 2.0 ** -5
+    s64[..., 1] = 2.0 ** -5
+    q = torch.full((1, 1, d), 2.0 ** 60, dtype=dtype, device=dev)
+    out = ops.cached_attention(q, cache, scales, i32(table, dev), i32([n], dev))[0, 0].cpu().double().numpy()
+    v = np.concatenate([values[b, 0, 1] * 2.0 ** -5 for b in table[0] if b >= 0])[:n]
+    half = torch.finfo(dtype).eps / 2 + 2.0 ** -20   # the output's rounding, the sums'
+    assert (out <= v.max(0) + half * np.abs(v).max(0)).all() and (out >= v.min(0) - half * np.abs(v).max(0)).all()
+    assert n > 1 or (np.abs(out - v[0]) <= half * np.abs(v[0])).all()
+    assert np.abs(out).max() > 0
