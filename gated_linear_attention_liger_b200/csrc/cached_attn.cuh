@@ -113,6 +113,7 @@ struct Args {
   float scale_log2;         // log2(e) / sqrt(d)
   int B, n_q, Hq, Hkv, G, width, n_blocks, lbs;   // blocks of 2^lbs tokens
   int rows, row_tiles;                            // rows = n_q * G
+  int inject_stall;         // test switch: the first CTA's first tile is never announced, so that waits run out
   Divisor by_ctas, by_units, by_row_tiles, by_G;  // units = Hkv * row_tiles
 };
 constexpr int kMaxRows = 16;           // query rows of a unit
@@ -443,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2)
           }
         }
         __syncwarp();
-        if (mine && in_tile == 0) mbar_arrive(&full[at]);
+        if (mine && in_tile == 0 && !(a.inject_stall && cta == 0 && pb == p0 && at == 0)) mbar_arrive(&full[at]);
       };
       // up to n of the tiles to do
       auto take = [&](int n) {

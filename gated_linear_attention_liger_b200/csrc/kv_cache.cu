@@ -346,6 +346,7 @@ liger_status liger_attn_cached(const void* q, const void* cache, const float* sc
   a.split = reinterpret_cast<liger::ca::Split*>(ws + L.off_split);
   a.err = static_cast<uint32_t*>(err);
   a.wait_ns = liger::bounded_wait_ns();
+  a.inject_stall = liger::take_injected_stall() ? 1 : 0;
   a.qstride = (long)q_stride;
   a.scale_log2 = 1.4426950408889634f / std::sqrt((float)d);
   a.B = B;

@@ -9,6 +9,8 @@ Scenarios:
                         next call on the same context is correct.
   noalloc_stall_status  the same through liger_attn_prefill_noalloc and
                         liger_attn_prefill_noalloc_status.
+  cached_stall          LIGER_TEST_INJECT_STALL=2: a short and a long cached attention call
+                        time out, each is reported once, and later calls are correct.
   general_parity        LIGER_PREFILL_PATH=general: the general (CUDA-core)
                         prefill kernel on bf16 cases against the oracle.
 """
@@ -96,6 +98,42 @@ def _noalloc_stall_status():
     print("no-alloc timeout reported and cleared")
 
 
+def _cached_stall():
+    import numpy as np
+    import torch
+
+    from gated_linear_attention_liger_b200 import ops
+    from tests import kv_reference as ref
+
+    dev = torch.device("cuda:0")
+    rng = np.random.default_rng(47)
+    # few tiles (the producer is done before the waits run out), and more of a CTA than its stages hold
+    calls = []
+    for n, Hkv in ((20, 1), (20000, 8)):
+        d, bs = 128, 64
+        c = ops.kv_cache_new(-(-n // bs), Hkv, d, bs, 1, n, dtype=torch.int8, device=dev)
+        k, v = (torch.tensor(rng.normal(size=(n, Hkv, d))).to(torch.bfloat16).to(dev) for _ in "kv")
+        ops.kv_cache_append(k, v, torch.arange(n, dtype=torch.int32, device=dev), c["cache"], c["scales"])
+        table = torch.arange(-(-n // bs), dtype=torch.int32, device=dev)[None]
+        q = torch.tensor(rng.normal(size=(1, 1, 4 * Hkv, d))).to(torch.bfloat16)
+        want = ref.attention(q.double().numpy(), ref.decode(c["cache"]), c["scales"].cpu().double().numpy(), table.cpu().numpy(), [n])
+        calls.append(((q.to(dev), c["cache"], c["scales"], table, torch.full((1,), n, dtype=torch.int32, device=dev)), want))
+    for args, _ in calls:   # the first two calls keep a tile back
+        ops.cached_attention(*args)
+        torch.cuda.synchronize()
+        assert ops.cached_attention_status() == ops.LIGER_ERR_TIMEOUT
+        msg = ops.last_error()
+        assert "gave up waiting" in msg and any(f"role {r}," in msg for r in (1, 2, 4)), msg
+        assert ops.cached_attention_status() == ops.LIGER_OK   # reported once
+    for args, want in calls:
+        out = ops.cached_attention(*args)
+        torch.cuda.synchronize()
+        assert ops.cached_attention_status() == ops.LIGER_OK
+        got = out.cpu().double().numpy()
+        assert (np.abs(got - want[0]) <= ref.attention_tolerance(want, torch.bfloat16, 128)).all()
+    print("cached attention timeouts reported:", msg)
+
+
 def _general_parity():
     import numpy as np
     import torch
@@ -115,6 +153,7 @@ def _general_parity():
 
 
 SCENARIOS = {"stall_then_recover": _stall_then_recover, "noalloc_stall_status": _noalloc_stall_status,
+             "cached_stall": _cached_stall,
              "general_parity": _general_parity}
 
 if __name__ == "__main__":

@@ -17,3 +17,9 @@ pytestmark = pytest.mark.gpu
 def test_bounded_wait_reports_timeout_and_context_survives(cuda_device):
     out = child_scenarios.run("stall_then_recover", child_scenarios.STALL_ENV)
     assert "timeout reported" in out
+
+
+def test_cached_attention_reports_timeouts_and_context_survives(cuda_device):
+    """The same for the cached attention, whose first two calls never announce the first CTA's first tile."""
+    out = child_scenarios.run("cached_stall", {**child_scenarios.STALL_ENV, "LIGER_TEST_INJECT_STALL": "2"})
+    assert "cached attention timeouts reported" in out
