@@ -681,3 +681,14 @@ def test_attention_scores_of_huge_magnitude(n, dtype, cuda_device):
     assert (out <= v.max(0) + half * np.abs(v).max(0)).all() and (out >= v.min(0) - half * np.abs(v).max(0)).all()
     assert n > 1 or (np.abs(out - v[0]) <= half * np.abs(v[0])).all()
     assert np.abs(out).max() > 0
+
+
+@pytest.mark.parametrize("n,want", [(16, 3 * 16), (33, -1), (48, 3 * 16)])
+def test_assign_next_token_beside_malformed_entries(n, want, cuda_device):
+    """A token that starts a block takes it from the ring, whatever stood in the row; one inside a block whose entry is
+    no block number has no slot."""
+    dev = cuda_device
+    slots, _, lens, span = ops.kv_cache_assign(i32([1], dev), i32([n], dev), i32([[5, -1, 99, 3]], dev), i32([3] + [0] * 7, dev),
+                                               i32([0, 1], dev), 16, 1)
+    assert slots.tolist() == [want] and lens.tolist() == [n + 1]
+    assert span.tolist() == ([1, 0] if n % 16 == 0 else [0, 1])
