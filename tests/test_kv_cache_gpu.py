@@ -692,3 +692,76 @@ def test_assign_next_token_beside_malformed_entries(n, want, cuda_device):
                                                i32([0, 1], dev), 16, 1)
     assert slots.tolist() == [want] and lens.tolist() == [n + 1]
     assert span.tolist() == ([1, 0] if n % 16 == 0 else [0, 1])
+
+
+def _half_steps(c, blocks, offs):
+    """What the codes of tokens at (blocks, offs) may be off by: half a step under their block's scale, [n, Hkv, 2, d].
+    A code that was rounded again when its scale grew is off by half a step of each of its scales, which are powers of two
+    below one another: at most twice the last one's for int8.  An e4m3 code keeps its three fraction bits in that, until it
+    is subnormal, so its steps add up to no more than those of a value twice as large."""
+    scale = c["scales"][blocks].double()[..., None]
+    if c["cache"].dtype == INT8:
+        return scale.expand(-1, -1, -1, c["cache"].shape[-1])
+    code = c["cache"].view(torch.uint8)[blocks, :, :, offs].view(E4M3).double().abs()
+    e = torch.clamp(torch.frexp(code)[1] - 1, min=-6)
+    return 2 * torch.exp2(e.double() - 4) * scale
+
+
+@pytest.mark.parametrize("kv", [E4M3, INT8], ids=["e4m3", "int8"])
+def test_cached_attention_agrees_with_the_prompt_attention(kv, cuda_device):
+    """The newest four tokens of prompts, appended and attended over the cache, against the causal attention over the
+    unquantised keys and values, and a token more against 64 bits: within what the codes' half steps can move."""
+    rng = np.random.default_rng(31)
+    dev, Hq, Hkv, d, bs, lens, nq = cuda_device, 8, 2, 64, 16, [100, 33, 64], 4
+    N, B = sum(lens), len(lens)
+    q = torch.tensor(rng.normal(size=(1, N, Hq, d)) * 0.25).to(BF16).to(dev)
+    k = torch.tensor(rng.normal(size=(1, N, Hkv, d))).to(BF16).to(dev)
+    around = rng.choice([-2.0, 2.0], (B, Hkv, d))   # what a sequence's and head's values lie around, far from the others'
+    v = torch.tensor(np.repeat(around, lens, 0)[None] + 0.5 * rng.normal(size=(1, N, Hkv, d))).to(BF16).to(dev)
+    cu = np.cumsum([0] + lens)
+    full = ops.full_causal_attention(q, k, v, cu_seqlens=i32(cu, dev))[0].double()
+    c = ops.kv_cache_new(20, Hkv, d, bs, B, 160, dtype=kv, device=dev)
+    state = (c["seq_lens"], c["block_table"], c["free_blocks"], c["free_span"])
+    put = dict(seq_lens_out=c["seq_lens"], free_span_out=c["free_span"])
+    slots = ops.kv_cache_assign(i32(lens, dev), *state, bs, N, **put)[0]
+    ops.kv_cache_append(k[0], v[0], slots, c["cache"], c["scales"])
+    newest = torch.stack([q[0, cu[s + 1] - nq:cu[s + 1]] for s in range(B)])
+    out = ops.cached_attention(newest, c["cache"], c["scales"], c["block_table"], c["seq_lens"]).double()
+
+    def check(got, ks, vs, qs, sl, what, plain=None):
+        """got [n, Hq, d], the last n queries qs of a sequence with keys ks, values vs [T, Hkv, d] and slots sl."""
+        T, n, G = ks.shape[0], qs.shape[0], Hq // Hkv
+        half = _half_steps(c, sl.long() // bs, sl.long() % bs)                          # [T, Hkv, 2, d]
+        held = c["cache"].view(torch.uint8)[sl.long() // bs, :, :, sl.long() % bs].view(kv).double() * c["scales"][sl.long() // bs].double()[..., None]
+        assert ((held - torch.stack([ks, vs], 2)).abs() <= half).all(), what
+        kd, vd, hk, hv = (x.repeat_interleave(G, 1) for x in (ks, vs, half[:, :, 0], half[:, :, 1]))
+        mask = torch.arange(T, device=dev) > (T - n + torch.arange(n, device=dev))[:, None]
+        x = torch.einsum("nhd,thd->hnt", qs, kd) / d ** 0.5
+        w = torch.softmax(x.masked_fill(mask, -np.inf), -1)
+        o, spread = torch.einsum("hnt,thd->nhd", w, vd), torch.einsum("hnt,thd->nhd", w, vd.abs())
+        # token j's score moves by at most move_j either way, so that its weight grows at most by a factor of e^move_j A and
+        # falls at most by its inverse, with A = sum_i w_i e^move_i (their sum falls at most by 1 / A: sum_i w_i e^-move_i is
+        # no less, by the means' inequality); then the values move by their half steps
+        grown = w * torch.exp(torch.einsum("nhd,thd->hnt", qs.abs(), hk) / d ** 0.5)
+        grown = grown * grown.sum(-1, keepdim=True)
+        tol = torch.einsum("hnt,thd->nhd", grown - w, vd.abs()) + torch.einsum("hnt,thd->nhd", grown, hv)
+        tol = tol + 2.0 ** -7 * (spread + tol)   # weights in bf16 or fp16 and the output's rounding, in either kernel: 2^-8 and less each
+        assert ((got - o).abs() <= tol).all(), what
+        assert tol.mean() < 0.5 * vd.abs().mean(), "the bound says something"
+        if plain is not None:
+            assert ((got - plain).abs() <= 2 * tol).all() and ((plain - o).abs() <= tol).all(), what
+
+    kd, vd, qd = k[0].double(), v[0].double(), q[0].double()
+    for s in range(B):
+        a, b = int(cu[s]), int(cu[s + 1])
+        check(out[s], kd[a:b], vd[a:b], qd[b - nq:b], slots[a:b], f"prompt {s}", full[b - nq:b])
+    # one more token each
+    q1 = torch.tensor(rng.normal(size=(B, Hq, d)) * 0.25).to(BF16).to(dev)
+    k1, v1 = (torch.tensor(x).to(BF16).to(dev) for x in (rng.normal(size=around.shape), around + rng.normal(size=around.shape)))
+    more = ops.kv_cache_assign(i32([1] * B, dev), *state, bs, B, **put)[0]
+    ops.kv_cache_append(k1, v1, more, c["cache"], c["scales"])
+    out = ops.cached_attention(q1, c["cache"], c["scales"], c["block_table"], c["seq_lens"]).double()
+    for s in range(B):
+        a, b = int(cu[s]), int(cu[s + 1])
+        check(out[s][None], torch.cat([kd[a:b], k1[s][None].double()]), torch.cat([vd[a:b], v1[s][None].double()]), q1[s][None].double(),
+              torch.cat([slots[a:b], more[s:s + 1]]), f"step {s}")
