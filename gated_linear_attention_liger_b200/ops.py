@@ -510,6 +510,11 @@ def kv_cache_assign(new_lens, seq_lens, block_table, free_blocks, free_span, blo
     slot map (at least the sum of the new lengths; the rest is -1).  seq_lens_out and free_span_out may be
     seq_lens and free_span (the state then advances in place).  Returns (slot_map [n_slots], cu_new [B + 1],
     seq_lens_out, free_span_out).
+
+    Lengths only grow, or end: do not lower seq_lens over a block border, the blocks behind it would be
+    lost.  Where drafted tokens may be turned down, assign all of them into new seq_lens_out and
+    free_span_out, append and attend; then assign the kept ones from the same seq_lens and free_span
+    as before, and append those again.
     """
     lib = load()
     if new_lens.dim() != 1 or block_table.dim() != 2 or free_blocks.dim() != 1:

@@ -374,6 +374,15 @@ typedef enum { LIGER_KV_E4M3 = 0, LIGER_KV_INT8 = 1 } liger_kv_dtype;
  *   seq_lens_out [B], free_span_out [2]  int32 (out)  the state after the call; may be
  *                seq_lens and free_span themselves.
  * A call on the same seq_lens and free_span (not overwritten) gives the same result again.
+ *
+ * Lengths only grow, or end.  A caller that lowers an entry of seq_lens itself may not change its
+ * ceil(len / block_size): the blocks behind the new length would be in no row and not in the
+ * ring, and lost to the cache.  Drafted tokens of which some are turned down are served by two
+ * calls: one with all drafts, into other seq_lens_out and free_span_out than the state; when
+ * they have been appended, attended and judged, another one on the same seq_lens and free_span
+ * with the number of kept ones, which gives the turned down ones' blocks back.  The kept tokens
+ * are then appended again, since their blocks may be others than before.  (A scale that a
+ * turned down token raised in a begun block stays.)
  */
 liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_lens, int32_t* block_table,
                                    int32_t* free_blocks, const int32_t* free_span, int32_t* slot_map, int32_t* cu_new,

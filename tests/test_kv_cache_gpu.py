@@ -765,3 +765,48 @@ def test_cached_attention_agrees_with_the_prompt_attention(kv, cuda_device):
         a, b = int(cu[s]), int(cu[s + 1])
         check(out[s][None], torch.cat([kd[a:b], k1[s][None].double()]), torch.cat([vd[a:b], v1[s][None].double()]), q1[s][None].double(),
               torch.cat([slots[a:b], more[s:s + 1]]), f"step {s}")
+
+
+@pytest.mark.parametrize("kv", [E4M3, INT8], ids=["e4m3", "int8"])
+def test_drafted_tokens_that_are_turned_down(kv, cuda_device):
+    """Steps of up to four drafted tokens a sequence, of which some are kept: the drafts are assigned into new lengths and a
+    new span, appended and attended; then the kept ones are assigned again from the old state, which gives the turned down
+    ones' blocks back, and appended again.  No block is ever lost or in two rows, and the cache stays the kept tokens'."""
+    rng = np.random.default_rng(32)
+    dev, B, Hq, Hkv, d, bs, width = cuda_device, 6, 4, 2, 64, 16, 6
+    n_blocks = B * width
+    c = ops.kv_cache_new(n_blocks, Hkv, d, bs, B, width * bs, dtype=kv, device=dev)
+    table, lens, span = c["block_table"], c["seq_lens"], c["free_span"]
+    held = [[] for _ in range(B)]   # the kept tokens' keys and values
+    for step in range(40):
+        new = rng.integers(0, 5, B) if step else rng.integers(1, 40, B)
+        if step and step % 7 == 0:
+            new[step % B] = -1
+        new = np.where(lens.cpu().numpy() + new > width * bs, -1, new)
+        count = np.maximum(new, 0)
+        kept = np.where(new < 0, -1, rng.integers(0, count + 1)) if step else new
+        N = int(count.sum())
+        k, v = (torch.tensor(rng.normal(size=(N, Hkv, d))).to(BF16).to(dev) for _ in "kv")
+        slots, cu, drafted, _ = ops.kv_cache_assign(i32(new, dev), lens, table, c["free_blocks"], span, bs, N)
+        ops.kv_cache_append(k, v, slots, c["cache"], c["scales"])
+        q = torch.tensor(rng.normal(size=(B, 4, Hq, d))).to(BF16)
+        out = ops.cached_attention(q.to(dev), c["cache"], c["scales"], table, drafted)
+        want = ref.attention(q.double().numpy(), ref.decode(c["cache"]), c["scales"].cpu().double().numpy(), table.cpu().numpy(), drafted.tolist())
+        _close(out, want, BF16, d, f"drafts of step {step}")
+        # the kept ones, from the same lengths and span as before
+        at = np.concatenate([cu[s].item() + np.arange(max(kept[s], 0)) for s in range(B)]).astype(int)
+        slots, _, lens, span = ops.kv_cache_assign(i32(kept, dev), lens, table, c["free_blocks"], span, bs, len(at))
+        ops.kv_cache_append(k[at], v[at], slots, c["cache"], c["scales"])
+        assert (slots >= 0).all()
+        for s in range(B):
+            held[s] = [] if kept[s] < 0 else held[s] + [torch.stack([k[cu[s] + i], v[cu[s] + i]], 1).double() for i in range(kept[s])]
+        assert lens.tolist() == [len(x) for x in held]
+        used = [int(table[s, j]) for s in range(B) for j in range(-(-len(held[s]) // bs))]
+        head, free = span.tolist()
+        assert sorted(used + [int(c["free_blocks"][(head + i) % n_blocks]) for i in range(free)]) == list(range(n_blocks)), step
+        for s in range(B):
+            if held[s]:
+                pos = torch.arange(len(held[s]), device=dev)
+                blk, off = table[s, pos // bs].long(), pos % bs
+                got = c["cache"].view(torch.uint8)[blk, :, :, off].view(kv).double() * c["scales"][blk].double()[..., None]
+                assert ((got - torch.stack(held[s])).abs() <= _half_steps(c, blk, off)).all(), step
