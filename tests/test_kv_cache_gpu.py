@@ -810,3 +810,37 @@ def test_drafted_tokens_that_are_turned_down(kv, cuda_device):
                 blk, off = table[s, pos // bs].long(), pos % bs
                 got = c["cache"].view(torch.uint8)[blk, :, :, off].view(kv).double() * c["scales"][blk].double()[..., None]
                 assert ((got - torch.stack(held[s])).abs() <= _half_steps(c, blk, off)).all(), step
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_attention_nonfinite_queries_stay_in_their_rows(d, dtype, cuda_device):
+    """A NaN or an infinity in one query row reaches no other row of its unit, not even of its own token or head."""
+    rng = np.random.default_rng(33)
+    dev, lens, nq, G, bs = cuda_device, [40, 3000, 2], 4, 4, 16
+    cache, scales, table, values, s64 = _attention_case(rng, lens, 1, bs, d, E4M3, dev)
+    q = torch.tensor(rng.normal(size=(3, nq, G, d))).to(dtype)
+    want = ref.attention(q.double().numpy(), values, s64, table, lens)
+    bad = np.zeros((3, nq, G), bool)
+    for s, i, h, x in ((0, 1, 2, "nan"), (1, 0, 0, "inf"), (1, 3, 3, "nan"), (2, 3, 1, "-inf")):
+        q[s, i, h, 5] = float(x)
+        bad[s, i, h] = True
+    out = ops.cached_attention(q.to(dev), cache, scales, i32(table, dev), i32(lens, dev))
+    keep = np.where(bad[..., None], 0.0, 1.0)
+    got = torch.where(torch.tensor(bad, device=dev)[..., None], torch.zeros_like(out), out)
+    _close(got, tuple(w * (keep if w.ndim == 4 else keep[..., 0]) for w in want), dtype, d)
+    assert out[0, 1, 2].isnan().all() and out[1, 3, 3].isnan().all()
+
+
+@pytest.mark.parametrize("nq,Hq,Hkv,d,dtype", [(16, 4096, 1, 64, BF16), (3, 1000, 1, 128, FP32), (1, 4096, 4096, 64, BF16)])
+def test_attention_most_rows_and_heads(nq, Hq, Hkv, d, dtype, cuda_device):
+    """The largest numbers of rows a kv head, and thousands of kv heads: sampled rows against 64 bits."""
+    rng = np.random.default_rng(34)
+    dev, lens, bs = cuda_device, [37, 0, 90], 16
+    cache, scales, table, values, s64 = _attention_case(rng, lens, Hkv, bs, d, INT8, dev)
+    q = torch.tensor(rng.normal(size=(3, nq, Hq, d))).to(dtype)
+    out = ops.cached_attention(q.to(dev), cache, scales, i32(table, dev), i32(lens, dev))
+    assert not out[1].any()
+    for h in [0, Hq - 1] + [int(x) for x in rng.integers(0, Hq, 6)]:
+        g = h // (Hq // Hkv)
+        _close(out[:, :, h:h + 1], ref.attention(q[:, :, h:h + 1].double().numpy(), values[:, g:g + 1], s64[:, g:g + 1], table, lens), dtype, d)
