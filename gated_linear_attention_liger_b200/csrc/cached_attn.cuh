@@ -44,11 +44,12 @@
 // Roundings to fewer bits: p to fp16 (2^-11 of itself; fp32 outputs: two terms, 2^-22), the output to its type.
 //
 // Measured on a B200 (calls back to back in a CUDA graph; bytes of the cache, queries and outputs over the 6570 GB/s of a
-// copy): 64 sequences of 2048 to 8192 tokens, Hq 32, Hkv 8, d 128, e4m3: 114.8 us, 0.89 of it (the copies without the
-// products took as long: the stream bounds it); one of 131072 tokens: 49.4 us, 0.83; 256 of up to 1500 tokens in blocks of 16,
-// int8: 82.2 us, 0.74; 4 new tokens each for 32 sequences of up to 6000, d 64: 33.8 us, 0.45 (16 rows a unit: the consumers'
-// latencies bound it, two warps a scheduler at 168 registers; 32 rows a unit spilled and took 117 us where two units of 16
-// take 71); one of 1000 tokens: 8.0 us, of latencies (the first tile comes after 2.5, its products take 1, its output 1.5,
+// copy): 64 sequences of 2048 to 8192 tokens, Hq 32, Hkv 8, d 128, e4m3: 115.0 us, 0.89 of it (the copies without the
+// products took as long: the stream bounds it); one of 131072 tokens: 49.8 us, 0.82; 256 of up to 1500 tokens in blocks of 16,
+// int8: 83.5 us, 0.73; 4 new tokens each for 32 sequences of up to 6000, d 64: 34.6 us, 0.44 (16 rows a unit: the consumers'
+// latencies bound it, two warps a scheduler at 157 registers; 32 rows a unit spilled and took 117 us where two units of 16
+// take 72), and for 32 of 2000 to 6000, d 128: 73.7 us, 0.55 (the same, and 16 rows at d 128 spill: bf16 96 bytes of stack,
+// fp32 up to 248); one of 1000 tokens: 8.3 us, of latencies (the first tile comes after 2.5, its products take 1, its output 1.5,
 // the join 3).
 #pragma once
 
@@ -74,7 +75,7 @@ constexpr int kWarps = 4;              // consumer warps
 constexpr int kThreads = 32 * (kWarps + 2);   // and the producer's and the output's warp
 constexpr int kEarly = 2;              // tiles that a stretch starts with before their scales have come
 constexpr int kJoinThreads = 256;
-constexpr int kJoinLanes = 8;         // at most, for a piece of a joined unit (16: one short sequence 9.6 instead of 8.9 us)
+constexpr int kJoinLanes = 8;         // at most, for a piece of a joined unit (16 took 0.7 us more on one short sequence)
 constexpr float kNoRef = -3e38f;       // reference of a row that has seen nothing: below every finite score
 constexpr float kRefBelow = 7.f;       // the reference is set this far below the maximum,
 constexpr float kRaiseAt = 15.f;       // and raised when a score exceeds it by this much

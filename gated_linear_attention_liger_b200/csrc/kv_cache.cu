@@ -236,7 +236,8 @@ liger_status liger_kv_cache_assign(const int32_t* new_lens, const int32_t* seq_l
     e = launch_assign<true, true>(a, 1, s);
   } else {
     const long long ctas = ((long long)n_slots + 4 * liger::kvc::kAssignThreads - 1) / (4 * liger::kvc::kAssignThreads);
-    const long long most = 2LL * liger::device_sm_count();   // (they are all resident: each scans all sequences)
+    const long long most = 2LL * liger::device_sm_count();   // (each scans all sequences; all resident up to 7000 of them, above
+                                                             // that their sums leave room for one CTA an SM, and half run later)
     const int n = (int)(ctas < most ? ctas : most);
     liger::mark_dominant_start(s);
     if (seq_lens_out != seq_lens && free_span_out != free_span) {

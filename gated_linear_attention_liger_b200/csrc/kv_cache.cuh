@@ -89,7 +89,7 @@ inline size_t assign_smem_bytes(int B) { return sizeof(int32_t) * (4 * (size_t)B
 // depends on another.  With STATE (the first CTA), it writes the offsets, lengths and span; where they stand in the
 // inputs' place, that is one CTA's work, in the same launch or in a later one.
 // What bounds it: latency.  The lengths, a scan and one dependent table or ring read; for millions of slots also their
-// write.  Measured on a B200: 64 sequences, a token each: 4.6 us; 512 prompts, 4.4 million slots (17.6 MB): 14.0 us (a
+// write.  Measured on a B200: 64 sequences, a token each: 4.6 us; 512 prompts, 4.4 million slots (17.6 MB): 14.1 us (a
 // grid of four CTAs an SM, which scanned in waves, took 31.7; sixteen tokens a lane written by that lane 21).
 template <bool SLOTS, bool STATE>
 __global__ void __launch_bounds__(kAssignThreads, 2) assign_kernel(AssignArgs a) {
@@ -439,8 +439,9 @@ __device__ __forceinline__ void requantise(uint8_t* half, int rows, float old, f
 // the rows before it are then requantised under the new one.
 // What bounds it: HBM for prompts (one read, one write); latency for single tokens.
 // Measured on a B200 against the 6570 GB/s of a copy: two prompts of 8192 tokens (Hkv 8, d 128, bf16, blocks of 64)
-// 19.9 us, 0.77 of it; nine ragged ones into blocks of 32 that have begun, int8: 37.3 us, 0.93; fp32, d 64, blocks of 16,
-// four of up to 2048: 10.1 us, 0.55 (two short waves of CTAs); a token each for 64 sequences: 2.7 us.  A CTA for each
+// 20.2 us, 0.76 of it; nine ragged ones into blocks of 32 that have begun, int8: 37.3 us, 0.93; fp32, d 64, blocks of 16,
+// four of up to 2048: 10.1 us, 0.55 (two short waves of CTAs, and 64 registers are too few for fp32: 88 to 144 bytes of
+// stack); a token each for 64 sequences: 2.7 us.  A CTA for each
 // run's keys and values whatever their size, with the finite test at each element, took 37.5, 69.1 and 14.0 us.
 template <typename Tin, int D, int BS>
 struct AppendShape {

@@ -601,7 +601,10 @@ def cached_attention(q, cache, scales, block_table, seq_lens, out=None, workspac
 
     q [B, Hq, d], or [B, n_q, Hq, d] for n_q <= 16 new tokens a sequence (bf16 or fp32; tokens may be
     evenly strided); cache, scales, block_table [B, width] and seq_lens [B] as for `kv_cache_append`, seq_lens
-    with the new tokens counted.  workspace: uint8 CUDA tensor of cached_attention_workspace_size(d)
+    with the new tokens counted.  Query i is the token len - n_q + i: a sequence with fewer new tokens has
+    their queries last, and the rows before them can be left aside (zeros before its first token).  fp32
+    queries and weights keep 22 bits (two fp16 terms), bf16 calls round weights to fp16.
+    workspace: uint8 CUDA tensor of cached_attention_workspace_size(d)
     bytes (allocated here when None).  Returns out in q's shape.
     """
     lib = load()

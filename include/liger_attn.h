@@ -32,7 +32,8 @@
  *     safe as long as they do not share output buffers.
  *   - dt is the storage type of q, k, v, out and the window ring.  The
  *     recurrent state is always fp32.  Arithmetic is fp32 (bf16 tensor-core
- *     operands with fp32 accumulation on the bf16 prefill path).
+ *     operands with fp32 accumulation on the bf16 prefill path; fp16 operands
+ *     in liger_attn_cached, whose section says what they keep).
  *   - Supported: d in {64, 128}; 1 <= w <= 64 (the bf16 tensor-core prefill
  *     needs w == 64 and an even Hq/Hkv and falls back to the general kernel
  *     otherwise); Hq % Hkv == 0; 0 <= alpha <= 1.
@@ -417,6 +418,10 @@ liger_status liger_kv_cache_append(const void* k, const void* v, const int32_t* 
  * A query that sees no token (len too short) gets zeros.  A table entry that is no block
  * number stands for tokens that are not there.  Slots behind a sequence's last token may
  * hold anything.
+ * Scores, softmax and sums are fp32 and codes exact.  What is held in fewer bits: bf16 calls
+ * round a token's weight to fp16 where it meets the value codes (2^-11 of itself; the sum of
+ * weights takes it unrounded); fp32 calls take queries and weights as two fp16 terms each, which
+ * keep 22 of their 24 bits.
  * Value scales of one sequence may differ as far as liger_kv_cache_append writes them (2^-64
  * for a block of zeros beside huge ones): with 2^e the largest, a token's weight counts down to
  * 2^(e - 133) of the largest weight (2^-33 at 2^100).
