@@ -41,7 +41,8 @@
 // takes log2(vs) as -64), so t is at most 2^79 and a sum of 2^31 of them finite, and in a sequence whose largest value scale is
 // 2^e a weight counts down to 2^(e - 133) of the largest (2^-33 at 2^100).  Rescaling and joining take a sum's factor in two
 // halves, since the references of a zero block (scale 2^-64) and its neighbour may lie more than 2^126 apart.
-// Roundings to fewer bits: p to fp16 (2^-11 of itself; fp32 outputs: two terms, 2^-22), the output to its type.
+// Roundings to fewer bits: p to fp16 (2^-11 of itself; fp32 outputs: two terms, 2^-22; either way up to 2^-25, which is 2^-32
+// of the row's largest p or less), the output to its type.
 //
 // Measured on a B200 (calls back to back in a CUDA graph; bytes of the cache, queries and outputs over the 6570 GB/s of a
 // copy): 64 sequences of 2048 to 8192 tokens, Hq 32, Hkv 8, d 128, e4m3: 115.0 us, 0.89 of it (the copies without the

@@ -421,7 +421,8 @@ liger_status liger_kv_cache_append(const void* k, const void* v, const int32_t* 
  * Scores, softmax and sums are fp32 and codes exact.  What is held in fewer bits: bf16 calls
  * round a token's weight to fp16 where it meets the value codes (2^-11 of itself; the sum of
  * weights takes it unrounded); fp32 calls take queries and weights as two fp16 terms each, which
- * keep 22 of their 24 bits.
+ * keep 22 of their 24 bits.  In both, a weight times its value scale is besides off by up to
+ * 2^-32 of the row's largest such product (fp16's subnormals).
  * Value scales of one sequence may differ as far as liger_kv_cache_append writes them (2^-64
  * for a block of zeros beside huge ones): with 2^e the largest, a token's weight counts down to
  * 2^(e - 133) of the largest weight (2^-33 at 2^100).
